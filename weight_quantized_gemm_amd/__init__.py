@@ -13,6 +13,13 @@ are settled once, and each call only enqueues the kernels (for tight loops).
     antiquant_matmul:  out = x1 @ ((x2 + offset) * scale) + bias + x3
     quant_matmul:      out = dequant_scale * pertoken_scale * (x1 @ x2 + bias) + x3
 
+What stands beside and between those projections in a serving step (``include/wqserve.h``)
+is in ``serve.py`` and reached from here too:
+
+    lora_matmul:       out[t] = x3[t] + scale[i] * (x1[t] @ a[i]^T) @ b[i]^T, i = indices[t]
+    rope:              rotary positions of q and k; k and v to rows of a cache
+    tree_attention:    attention of one, a chain or a tree of new tokens over a paged cache
+
 (the formulas of the aclnnWeightQuantMatmulAllReduce guide, section 计算公式, and of the
 aclnnQuantMatmulAllReduceV2 page, section Function, at one rank).
 """
@@ -28,7 +35,9 @@ __all__ = ["WQ_F16", "WQ_BF16", "WQ_F32", "WQ_I8", "WQ_I4", "WQ_I32", "WQ_F8E4M3
            "packed_weight_bytes",
            "WqError", "lib", "library_path", "make_desc", "antiquant_matmul",
            "antiquant_workspace_size", "quant_matmul", "quant_workspace_size", "AntiquantMatmul",
-           "QuantMatmul", "profile_next_call", "EXPORTS"]
+           "QuantMatmul", "profile_next_call", "EXPORTS",
+           "SERVE_EXPORTS", "WQ_ROPE_HALF", "WQ_ROPE_INTERLEAVED", "LoraMatmul", "lora_matmul", "Rope", "rope",
+           "rope_frequencies", "TreeAttention", "tree_attention", "tree_mask_from_parents"]
 
 WQ_F16, WQ_BF16, WQ_F32, WQ_I8, WQ_I4, WQ_I32, WQ_F8E4M3 = 1, 2, 3, 4, 5, 6, 7
 WQ_OK, WQ_ERR_PARAM_NULLPTR, WQ_ERR_PARAM_INVALID, WQ_ERR_RUNTIME = 0, 161001, 161002, 561001
@@ -75,6 +84,13 @@ def declare(L):
         "wq_profile_next_call": ([ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
         "wq_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "wq_version": ([], ctypes.c_int),
+        # wqserve.h
+        "wq_lora_matmul_get_workspace_size": ([P] * 8 + [u64p], ctypes.c_int),
+        "wq_lora_matmul": ([P] * 8 + [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p], ctypes.c_int),
+        "wq_rope": ([P] * 6 + [ctypes.c_int32, ctypes.c_float] + [P] * 3 + [ctypes.c_void_p], ctypes.c_int),
+        "wq_tree_attention_get_workspace_size": ([P] * 7 + [ctypes.c_int64, P, u64p], ctypes.c_int),
+        "wq_tree_attention": ([P] * 7 + [ctypes.c_int64, ctypes.c_float, P, ctypes.c_void_p, ctypes.c_uint64,
+                                         ctypes.c_void_p], ctypes.c_int),
     }
     for name, (args, res) in sigs.items():
         if hasattr(L, name):
@@ -384,3 +400,8 @@ def quant_matmul(x1, x2, dequant_scale, pertoken_scale=None, bias=None, x3=None,
     with _alloc_on(stream, x1.device) as s:
         return QuantMatmul(x1, x2, dequant_scale, pertoken_scale, bias, x3, out_dtype=out_dtype, out=out,
                            acc_out=acc_out)(s)
+
+
+from .serve import (SERVE_EXPORTS, WQ_ROPE_HALF, WQ_ROPE_INTERLEAVED, LoraMatmul, Rope,  # noqa: E402
+                    TreeAttention, lora_matmul, rope, rope_frequencies, tree_attention,
+                    tree_mask_from_parents)

@@ -1,0 +1,53 @@
+// Planning of the serving operators: tile rows, splits and workspace sizes.  Host-only C++.
+// The plans are for an MI355X's 256 compute units and depend on shapes alone, so that a size
+// query answers without a device and a captured call keeps its workspace.
+#include <algorithm>
+
+#include "serve_problem.h"
+#include "serve_tile.h"
+
+namespace wq {
+namespace {
+
+constexpr int kCUs = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+LoraPlan plan_lora(const LoraProblem& p) {
+  LoraPlan pl;
+  pl.window = p.m <= kLoraSmallM ? 16 : 64;
+  pl.windows = ceil_div(p.m, pl.window);
+  // Side-by-side work items of a window: its rows may each have an adapter of their own.
+  const int64_t distinct = std::min<int64_t>({p.L + 1, p.m, pl.window});
+  pl.slots = (int)std::max<int64_t>(1, std::min<int64_t>(distinct, p.m <= 64 ? 16 : 4));
+  const int rank_blocks = (int)ceil_div(p.r, 16 * kLoraRankTiles);
+  const int64_t want = 2 * kCUs / std::max<int64_t>(1, pl.windows * rank_blocks);
+  int64_t splits = std::min<int64_t>({want, 16, ceil_div(p.k, 256)});
+  splits = std::max<int64_t>(1, splits);
+  pl.kchunk = (int)(ceil_div(ceil_div(p.k, splits), 64) * 64);
+  pl.splits = (int)ceil_div(p.k, pl.kchunk);
+  pl.workspace = p.m == 0 ? 0 : align256((int64_t)pl.splits * p.m * p.r * 4);
+  return pl;
+}
+
+TreePlan plan_tree(const TreeProblem& p) {
+  TreePlan pl;
+  if (p.N == 0 || p.B == 0) return pl;
+  // rows of the average sequence; a tile of too many rows only pads, one of too few reads
+  // the keys again
+  const int64_t rows = ceil_div(p.N, std::min(p.N, p.B)) * p.group;
+  pl.row_blocks = rows <= 16 || p.d == 256 ? 1 : rows <= 32 ? 2 : 4;
+  const int R = 16 * pl.row_blocks;
+  // tiles: each sequence with tokens has ceil(T_b * group / R) for each cached head
+  const int64_t tiles = (p.N * p.group / R + std::min(p.N, p.B)) * p.hkv;
+  const int64_t units = std::max<int64_t>(1, ceil_div((int64_t)p.width * p.page, tree_unit(p.d)));
+  pl.blocks = std::min<int64_t>(tree_max_blocks(p.d), tiles * units);
+  // two partial tiles for each workgroup: outputs, then (maximum, sum) of each row
+  pl.workspace = align256(pl.blocks * 2 * R * (int64_t)(p.d + 2) * 4);
+  return pl;
+}
+
+}  // namespace wq
