@@ -203,7 +203,7 @@ def test_tree_accepts(wqlib):
     # a workspace of some megabytes whatever the lengths
     for kw in (dict(N=1 << 24, B=65535, width=127, page=1 << 20, pages=2047), dict(N=64, B=1, width=1 << 17)):
         st, size = tree(wqlib, **tree_args(**kw))
-        assert st == OK and size <= 64 << 20
+        assert st == OK and size <= 66 << 20
 
 
 def test_tree_refuses(wqlib):

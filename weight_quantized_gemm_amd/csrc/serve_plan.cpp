@@ -36,17 +36,28 @@ LoraPlan plan_lora(const LoraProblem& p) {
 TreePlan plan_tree(const TreeProblem& p) {
   TreePlan pl;
   if (p.N == 0 || p.B == 0) return pl;
-  // rows of the average sequence; a tile of too many rows only pads, one of too few reads
-  // the keys again
+  // Rows of the average sequence: a tile of too many rows only pads, one of too few reads the
+  // keys again.
   const int64_t rows = ceil_div(p.N, std::min(p.N, p.B)) * p.group;
-  pl.row_blocks = rows <= 16 || p.d == 256 ? 1 : rows <= 32 ? 2 : 4;
-  const int R = 16 * pl.row_blocks;
-  // tiles: each sequence with tokens has ceil(T_b * group / R) for each cached head
-  const int64_t tiles = (p.N * p.group / R + std::min(p.N, p.B)) * p.hkv;
-  const int64_t units = std::max<int64_t>(1, ceil_div((int64_t)p.width * p.page, tree_unit(p.d)));
-  pl.blocks = std::min<int64_t>(tree_max_blocks(p.d), tiles * units);
-  // two partial tiles for each workgroup: outputs, then (maximum, sum) of each row
-  pl.workspace = align256(pl.blocks * 2 * R * (int64_t)(p.d + 2) * 4);
+  int per_cu = 1;  // workgroups that a compute unit holds: by LDS, and 8 waves of 256 registers
+  if (rows <= 32 || p.d == 256) {
+    pl.waves = tree_key_waves(p.d);
+    pl.rows = rows <= 16 || p.d == 256 ? 16 : 32;
+    pl.unit = 32 * pl.waves;
+    per_cu = p.d == 64 ? 2 : 1;
+  } else {
+    pl.split_rows = true;
+    pl.waves = rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
+    pl.rows = 32 * pl.waves;
+    pl.unit = tree_row_keys(pl.waves);
+    per_cu = 8 / pl.waves;
+  }
+  // tiles: each sequence with tokens has ceil(T_b * group / rows) for each cached head
+  const int64_t tiles = (p.N * p.group / pl.rows + std::min(p.N, p.B)) * p.hkv;
+  const int64_t units = std::max<int64_t>(1, ceil_div((int64_t)p.width * p.page, pl.unit));
+  pl.blocks = std::min<int64_t>(kCUs * per_cu, tiles * units);
+  // two partial tiles for each workgroup: outputs, then (base, sum) of each row
+  pl.workspace = align256(pl.blocks * 2 * pl.rows * (int64_t)(p.d + 2) * 4);
   return pl;
 }
 

@@ -79,8 +79,11 @@ struct TreeProblem {
 };
 
 struct TreePlan {
-  int row_blocks = 1;    // 16-row blocks of a work tile (rows = tokens x query heads of a cached head)
-  int64_t blocks = 0;    // workgroups (an upper bound of the work ranges)
+  bool split_rows = false;  // a workgroup's waves split the rows of a tile (else its keys)
+  int waves = 4;
+  int rows = 16;            // of a tile: tokens x query heads of a cached head
+  int unit = 128;           // keys, the unit of the work that workgroups share
+  int64_t blocks = 0;       // workgroups (an upper bound of the shares)
   int64_t workspace = 0;
 };
 

@@ -10,10 +10,7 @@ constexpr int64_t kLoraSmallM = 1024;  // up to here a window is 16 token rows, 
 constexpr int kLoraRankTiles = 4;      // 16-rank tiles that one workgroup of the first product computes
 
 // ---- tree attention
-constexpr int kTreeKeys = 32;                                      // keys of a wave's tile
-constexpr int tree_waves(int d) { return d == 256 ? 2 : 4; }       // waves of a workgroup, by head dim
-constexpr int tree_unit(int d) { return kTreeKeys * tree_waves(d); }  // keys of a workgroup's round
-// Workgroups that share the work: what the LDS lets reside on 256 compute units at once.
-constexpr int tree_max_blocks(int d) { return d == 64 ? 512 : 256; }
+constexpr int tree_key_waves(int d) { return d == 256 ? 2 : 4; }   // waves that split the keys, 32 to a tile
+constexpr int tree_row_keys(int waves) { return waves == 2 ? 32 : 64; }  // keys of a tile whose rows the waves split
 
 }  // namespace wq

@@ -3,28 +3,35 @@
 // token i sees.
 //
 // Work.  The tokens of a sequence and the G query heads of one cached head share that head's
-// keys, so they are the rows of one tile: row = token * G + query head, R = 16 * RT rows.  A
-// tile's keys are cut into units of 32 keys a wave, and all units of all tiles stand in one
-// row (sequence, cached head, tile, key).  Each workgroup takes an equal share of that row,
-// wherever it begins and ends: ragged lengths, few long sequences and many short ones load the
-// chip alike, without knowing a length on the host.  A tile that one workgroup holds whole is
-// written by it; one that is cut leaves partial results (output, maximum, sum) that a second
-// kernel joins in key order.  A workgroup has at most two such parts: its first and its last.
+// keys, so they are the rows of one tile: row = token * G + query head, R rows.  A tile's keys
+// are cut into units, and all units of all tiles stand in one row (sequence, cached head,
+// tile, key).  Each workgroup takes an equal share of that row, wherever it begins and ends:
+// ragged lengths, few long sequences and many short ones load the chip alike, without knowing a
+// length on the host.  A tile that one workgroup holds whole is written by it; one that is cut
+// leaves partial results (output, maximum, sum) that a second kernel joins in key order.  A
+// workgroup has at most two such parts: its first and its last.
 //
-// One wave's tile is 32 keys.  K and V go straight from memory to the wave's own LDS (16 bytes a
-// lane, two stages), so waves wait for nobody and the next tile is always in flight; the rows
-// of pages are found through slot numbers that the workgroup writes to LDS ahead, 2048 keys at a
-// time.
+// Two kernels, by the rows of the average sequence (plan_tree):
+//   keys: up to 32 rows, bound by memory.  The waves of a workgroup split the keys; each streams
+//     its own 32-key tiles through its own LDS and waits for nobody until they join at the end.
+//   rows: more rows, bound by the matrix cores and the exponentials.  The waves split the rows,
+//     32 each, and share every tile of K and V, so that a key is read from memory and into
+//     LDS once for up to 256 rows.
+// In both, K and V go straight from memory to LDS (16 bytes a lane, two stages); the rows of
+// pages are found through slot numbers that the workgroup writes to LDS ahead.
 //
 // S^T = K Q^T (keys as MFMA rows, query rows as columns): element i of lane l is key 4 (l / 16) +
 // i of row l % 16, so a row's maximum is two cross-lane steps away, its statistics stand in the
-// lanes that need them, and the lane's own 8 weights of a 32-key tile are, in this order, the B
+// lanes that need them, and the lane's own 8 weights of 32 keys are, in this order, the B
 // operand of O^T += V^T P^T, if V^T takes the keys in the same order: two transpose reads of 4
 // keys each.  The weights never leave the registers.
 //
-// Scores, maxima, sums and outputs are fp32 (base 2: scale * log2(e) is folded into the scores).
-// The weights, at most 1, are rounded to 16 bits for the second product: an error of
-// at most 2^-8 (bf16) or 2^-11 (fp16) of each, of the size of the result's own rounding.
+// Scores, sums and outputs are fp32 (base 2: scale * log2(e) is folded into the scores).  The
+// running base that is taken off a row's scores follows the maximum only when that has grown by
+// more than kSlack: weights then reach 2^kSlack instead of 1, which fp32 and both 16-bit types
+// hold, and the outputs are rescaled a few times in a whole row instead of in every tile.  The
+// weights are rounded to 16 bits for the second product: an error of at most 2^-8 (bf16) or
+// 2^-11 (fp16) of each, of the size of the result's own rounding.
 #include <algorithm>
 #include <cmath>
 
@@ -48,6 +55,7 @@ struct TreeArgs {
   int64_t pages;
   int32_t N, B, hq, hkv, group, width, words, has_mask;
   int32_t blocks;     // workgroups of the launch
+  int32_t R, unit;    // rows of a tile, keys of a unit
   FastDiv by_page, by_group;
   // The scores' factor, |scale| * log2(e), is positive, so that it neither turns the order of the
   // scores nor moves -inf; a negative scale flips the queries' signs, a zero one clears them.
@@ -55,7 +63,8 @@ struct TreeArgs {
   uint32_t q_and, q_xor;
 };
 
-constexpr int kSlots = 2048;  // keys whose slots stand in LDS at a time
+constexpr int kSlots = 1024;    // keys whose slots stand in LDS at a time
+constexpr float kSlack = 8.f;   // log2 of the largest weight
 constexpr float kNone = -__builtin_inff();
 
 // ------------------------------------------------------------------------------ the schedule
@@ -64,7 +73,6 @@ struct Seq {
   int tiles = 0, units = 0;                  // row tiles of a cached head, units of a tile
 };
 
-template <int R, int UNIT>
 __device__ __forceinline__ Seq sequence(const TreeArgs& a, int b) {
   Seq s;
   s.q0 = min(max(a.starts[b], 0), a.N);
@@ -72,8 +80,8 @@ __device__ __forceinline__ Seq sequence(const TreeArgs& a, int b) {
   s.ctx = max(a.context[b], 0);
   const int64_t len = (int64_t)s.ctx + s.tokens, most = a.pages ? (int64_t)a.width * a.by_page.d : 0;
   s.len = (int)min(len, most);
-  s.tiles = (int)(((int64_t)s.tokens * a.group + R - 1) / R);
-  s.units = max(1, (s.len + UNIT - 1) / UNIT);  // a tile without keys still writes zeros
+  s.tiles = (int)(((int64_t)s.tokens * a.group + a.R - 1) / a.R);
+  s.units = max(1, (s.len + a.unit - 1) / a.unit);  // a tile without keys still writes zeros
   return s;
 }
 
@@ -83,24 +91,22 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   return v;
 }
 
-template <int R, int UNIT>
 __device__ __forceinline__ int64_t total_units(const TreeArgs& a, int lane) {
   int64_t sum = 0;
   for (int b = lane; b < a.B; b += 64) {
-    const Seq s = sequence<R, UNIT>(a, b);
+    const Seq s = sequence(a, b);
     sum += (int64_t)s.tiles * s.units * a.hkv;
   }
   return wave_sum(sum);
 }
 
 // The sequence that holds unit u (u < total), and the number of units before it.
-template <int R, int UNIT>
 __device__ __forceinline__ int find_sequence(const TreeArgs& a, int lane, int64_t u, int64_t& before) {
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     int64_t own = 0;
     if (b0 + lane < a.B) {
-      const Seq s = sequence<R, UNIT>(a, b0 + lane);
+      const Seq s = sequence(a, b0 + lane);
       own = (int64_t)s.tiles * s.units * a.hkv;
     }
     int64_t upto = own;
@@ -127,13 +133,12 @@ __device__ __forceinline__ int64_t share_begin(int64_t total, int64_t n, int64_t
 // The share that holds unit u: the largest i with total * i / n <= u.
 __device__ __forceinline__ int64_t share_of(int64_t total, int64_t n, int64_t u) { return ((u + 1) * n - 1) / total; }
 
-// ------------------------------------------------------------------------------ one wave's tile
-template <int HD>
+// ------------------------------------------------------------------------------ a tile of keys
+template <int HD, int KT>
 struct Cfg {
-  static constexpr int NW = tree_waves(HD), UNIT = tree_unit(HD), CH = HD / 8, RB = HD * 2;
-  static constexpr int Half = kTreeKeys * RB, Stage = 2 * Half;  // K, then V
-  static constexpr int Loads = Half / 1024;                      // per tensor and tile, 1 KB each
-  static constexpr int Pad = HD + 4;                             // floats of a merge row
+  static constexpr int CH = HD / 8, RB = HD * 2;              // 16-byte chunks and bytes of a row
+  static constexpr int Half = KT * RB, Stage = 2 * Half;      // K, then V
+  static constexpr int Loads = Half / 1024;                   // per tensor and tile, 1 KB each
 };
 
 // 16-byte chunk c of K row r stands in slot row_slot (16-byte reads of 16 rows at one chunk hit all
@@ -148,21 +153,20 @@ template <int HD> __device__ __forceinline__ int v_chunk(int r, int c) {
   else return 2 * pair_slot<HD * 2>(r, c >> 1) + (c & 1);
 }
 
-template <int HD>
+// Load part `w` of `parts` of a tile: keys first + 0 .. KT - 1 of the slots in LDS.
+template <int HD, int KT, int PARTS>
 __device__ __forceinline__ void load_tile(const TreeArgs& a, const uint16_t* kh, const uint16_t* vh, const int* slots,
-                                          int first, int count, uint8_t* stage, int lane) {
-  using C = Cfg<HD>;
+                                          int first, int count, uint8_t* stage, int w, int lane) {
+  using C = Cfg<HD, KT>;
+  static_assert(C::Loads % PARTS == 0, "whole loads for each wave");
   asm volatile("" : "+v"(lane));  // addresses are made anew for each tile: kept, they would take 100 registers
+  stage += 1024 * (C::Loads / PARTS) * w;
+  const int e0 = 64 * (C::Loads / PARTS) * w + lane;
 #pragma unroll
-  for (int i = 0; i < C::Loads; ++i) {
-    const int e = i * 64 + lane, row = e / C::CH, c = e % C::CH;
+  for (int i = 0; i < C::Loads / PARTS; ++i) {
+    const int row = (e0 + 64 * i) / C::CH, c = (e0 + 64 * i) % C::CH;
     const uint32_t slot = (uint32_t)max(slots[min(first + row, count - 1)], 0);  // no such key: any row of the cache
     dma16_global((const uint8_t*)kh + (uint64_t)slot * a.k_row + 16 * k_chunk<HD>(row, c), stage + 1024 * i);
-  }
-#pragma unroll
-  for (int i = 0; i < C::Loads; ++i) {
-    const int e = i * 64 + lane, row = e / C::CH, c = e % C::CH;
-    const uint32_t slot = (uint32_t)max(slots[min(first + row, count - 1)], 0);
     dma16_global((const uint8_t*)vh + (uint64_t)slot * a.v_row + 16 * v_chunk<HD>(row, c), stage + C::Half + 1024 * i);
   }
 }
@@ -173,10 +177,50 @@ __device__ __forceinline__ bool not_finite(uint32_t half) {
   return (half & e) == e;
 }
 
+// Edge tiles hold keys that some row does not see: past the end, on no page, or drafted tokens.
+// The scores of unseen keys become -inf there, and V loses, for the matrix product, its rows
+// without a key and its infinities and NaN (0 * inf would reach rows that do not see them); what
+// those contribute to rows that do see them is added afterwards.
+
+// Bit r: whether key r of the tile exists (keys at or past `count` do not belong to this piece of work).
+template <int KT>
+__device__ __forceinline__ uint64_t tile_keys(const int* slots, int first, int count, int lane) {
+  return __ballot(lane < KT && first + lane < count && slots[min(first + lane, kSlots - 1)] >= 0);
+}
+
+// Part `w` of `parts` of V without what the product must not meet; returns the rows (bits) of this
+// part that held an infinity or NaN.
+template <int HD, bool BF16, int KT, int PARTS>
+__device__ __forceinline__ uint64_t clean_values(uint8_t* stage, uint64_t keys, int w, int lane) {
+  using C = Cfg<HD, KT>;
+  uint64_t odd = 0;
+#pragma unroll 1
+  for (int e = w * (KT * C::CH / PARTS) + lane; e < (w + 1) * (KT * C::CH / PARTS); e += 64) {
+    const int row = e / C::CH;
+    u32x4_t* at = (u32x4_t*)(stage + C::Half + 16 * e);
+    u32x4_t x = *at;
+    bool change = !((keys >> row) & 1);
+    if (change) x = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const bool lo = not_finite<BF16>(x[d]), hi = not_finite<BF16>(x[d] >> 16);
+      if (lo || hi) {
+        odd |= 1ull << row;
+        change = true;
+        x[d] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+      }
+    }
+    if (change) *at = x;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) odd |= (uint64_t)__shfl_xor((long long)odd, o, 64);
+  return odd;
+}
+
 // Which of the 32 keys from drafted token draft0 on (negative: the context's end) a token sees,
 // as far as the mask goes: 32 bits of its row of the mask, which two words hold.
 __device__ __forceinline__ uint32_t tile_bits(const TreeArgs& a, const Seq& s, int token, int draft0) {
-  if (draft0 <= -kTreeKeys) return ~0u;
+  if (draft0 <= -32) return ~0u;
   if (!a.has_mask) {  // drafted tokens 0 .. token
     const int last = token - draft0;
     return last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u;
@@ -188,236 +232,289 @@ __device__ __forceinline__ uint32_t tile_bits(const TreeArgs& a, const Seq& s, i
   return (uint32_t)(((hi << 32) | lo) >> shift);
 }
 
-// One 32-key tile (keys key0 + 0 .. 31, of which those at or past key_end do not belong to this
-// piece of work) for RT 16-row blocks.  EDGE tiles hold keys that some row does not see: past the end, on no
-// page, or drafted tokens.  There the scores of unseen keys become -inf, and V loses, for the
-// matrix product, its rows without a key and its infinities and NaN (0 * inf would reach rows
-// that do not see them); what those contribute to rows that do see them is added afterwards.
-template <int HD, bool BF16, int RT, bool EDGE>
-__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, int key0,
-                                             int key_end, uint8_t* stage, const uint16_t* vh, int lane,
-                                             const u32x4_t (&qf)[RT][HD / 32], const int (&token)[RT],
-                                             f32x4_t (&o)[RT][HD / 16], float (&m)[RT], float (&l)[RT]) {
-  using C = Cfg<HD>;
+// The maximum (or sum) of a value over the four lanes l % 16 + 16 * {0, 1, 2, 3}, in all of them.
+template <bool SUM>
+__device__ __forceinline__ float across(float v) {
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const float a = __uint_as_float(h[0]), b = __uint_as_float(h[1]);
+  v = SUM ? a + b : fmaxf(a, b);
+  const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const float c = __uint_as_float(q[0]), d = __uint_as_float(q[1]);
+  return SUM ? c + d : fmaxf(c, d);
+}
+
+// What a wave keeps of its RT 16-row blocks: queries (MFMA B operands), tokens, outputs
+// (transposed: element i of o[t][d] is column 16 d + 4 (l / 16) + i of row l % 16), bases and this
+// lane's part of the sums.
+template <int HD, int RT>
+struct Rows {
+  u32x4_t q[RT][HD / 32];
+  int token[RT];
+  f32x4_t o[RT][HD / 16];
+  float m[RT], l[RT];
+};
+
+template <int HD, bool BF16, int RT>
+__device__ __forceinline__ void start_rows(const TreeArgs& a, const Seq& s, int kvh, int row0, int rows, int lane,
+                                           Rows<HD, RT>& w) {
+  const int l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int row = min(row0 + 16 * t + l16, rows - 1);
+    w.token[t] = (int)divide((uint32_t)row, a.by_group);
+    const int head = kvh * a.group + row - w.token[t] * a.group;
+    const uint16_t* qr = a.q + (int64_t)(s.q0 + w.token[t]) * a.q_t + (int64_t)head * a.q_h + 8 * g;
+#pragma unroll
+    for (int j = 0; j < HD / 32; ++j) w.q[t][j] = (*(const u32x4_t*)(qr + 32 * j) & a.q_and) ^ a.q_xor;
+    w.m[t] = kNone;
+    w.l[t] = 0.f;
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d) w.o[t][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// A tile of KT keys for the rows of one wave.  EDGE tiles: `keys` of the tile that exist, `odd` rows of V
+// that clean_values took infinities or NaN from; draft0 is the drafted token of the tile's first key.
+template <int HD, bool BF16, int RT, int KT, bool EDGE>
+__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
+                                             uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
+                                             int lane, Rows<HD, RT>& w) {
+  using C = Cfg<HD, KT>;
+  constexpr int KB = KT / 16;
   asm volatile("" : "+v"(lane));  // as in load_tile
   const int l16 = lane & 15, g = lane >> 4;
-  f32x4_t sc[RT][2];
+  f32x4_t sc[RT][KB];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) sc[t][0] = sc[t][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int h = 0; h < KB; ++h) sc[t][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < HD / 32; ++j)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < KB; ++h) {
       const int row = 16 * h + l16;
       const u32x4_t kf = *(const u32x4_t*)(stage + row * C::RB + 16 * k_chunk<HD>(row, 4 * j + g));
 #pragma unroll
-      for (int t = 0; t < RT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, qf[t][j], sc[t][h]);
+      for (int t = 0; t < RT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, w.q[t][j], sc[t][h]);
     }
 
-  uint32_t seen[RT];      // EDGE: bit r, whether this lane's row sees key r of the tile
-  uint32_t odd_rows = 0;  // EDGE: keys whose V holds an infinity or NaN
+  uint32_t seen[RT][KT / 32];  // EDGE: bit r of word b, whether this lane's row sees key 32 b + r
   if constexpr (EDGE) {
-    const bool is_key = lane < kTreeKeys && key0 + lane < key_end && slots[min(first + lane, kSlots - 1)] >= 0;
-    const uint32_t keys = (uint32_t)__ballot(is_key);
-    const int draft0 = key0 - s.ctx;  // the drafted token of the tile's first key, negative in the context
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      seen[t] = keys & tile_bits(a, s, token[t], draft0);
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int b = 0; b < KT / 32; ++b) {
+        seen[t][b] = (uint32_t)(keys >> (32 * b)) & tile_bits(a, s, w.token[t], draft0 + 32 * b);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!((seen[t] >> (16 * h + 4 * g + i)) & 1)) sc[t][h][i] = kNone;
-    }
-#pragma unroll 1
-    for (int e = lane; e < kTreeKeys * C::CH; e += 64) {
-      const int row = e / C::CH;
-      u32x4_t* at = (u32x4_t*)(stage + C::Half + 16 * e);
-      u32x4_t x = *at;
-      bool change = !((keys >> row) & 1);
-      if (change) x = u32x4_t{0, 0, 0, 0};
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const bool lo = not_finite<BF16>(x[d]), hi = not_finite<BF16>(x[d] >> 16);
-        if (lo || hi) {
-          odd_rows |= 1u << row;
-          change = true;
-          x[d] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
-        }
+          for (int i = 0; i < 4; ++i)
+            if (!((seen[t][b] >> (16 * h + 4 * g + i)) & 1)) sc[t][2 * b + h][i] = kNone;
       }
-      if (change) *at = x;
-    }
-#pragma unroll
-    for (int w = 1; w < 64; w <<= 1) odd_rows |= (uint32_t)__shfl_xor((int)odd_rows, w, 64);
-    __builtin_amdgcn_wave_barrier();
   }
 
-  u32x4_t pf[RT];
+  u32x4_t pf[RT][KT / 32];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    float top = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
-                      fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float now = fmaxf(m[t], top * a.scale);
-    const float base = now == kNone ? 0.f : now;  // no key seen so far: every weight is 0
-    const float keep = __builtin_amdgcn_exp2f(m[t] - base);
-    m[t] = now;
+    float top = sc[t][0][0];
+#pragma unroll
+    for (int h = 0; h < KB; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][h][i]);
+    top = across<false>(top) * a.scale;
+    if (__ballot(top > w.m[t] + kSlack)) {
+      const float now = fmaxf(w.m[t], top);
+      const float keep = __builtin_amdgcn_exp2f(w.m[t] - (now == kNone ? 0.f : now));
+      w.m[t] = now;
+      w.l[t] *= keep;
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d) w.o[t][d] *= keep;
+    }
+    const float base = w.m[t] == kNone ? 0.f : w.m[t];  // no key seen so far: every weight is 0
     float sum = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < KB; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p = __builtin_amdgcn_exp2f(fmaf(sc[t][h][i], a.scale, -base));
         sc[t][h][i] = p;
         sum += p;
       }
-    l[t] = l[t] * keep + sum;
+    w.l[t] += sum;
 #pragma unroll
-    for (int d = 0; d < HD / 16; ++d) o[t][d] *= keep;
-    pf[t] = u32x4_t{pack2<BF16>(sc[t][0][0], sc[t][0][1]), pack2<BF16>(sc[t][0][2], sc[t][0][3]),
-                    pack2<BF16>(sc[t][1][0], sc[t][1][1]), pack2<BF16>(sc[t][1][2], sc[t][1][3])};
+    for (int b = 0; b < KT / 32; ++b)
+      pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
+                         pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
+                         pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
   }
 
-  // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3
+  // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3 of each 32
   const uint8_t* vs = stage + C::Half;
-  const int vrow = 4 * g + (l16 >> 2), vhalf = 8 * (l16 & 1);
+  const int vhalf = 8 * (l16 & 1);
 #pragma unroll
-  for (int d = 0; d < HD / 16; ++d) {
-    const int c = 2 * d + ((l16 & 3) >> 1);
-    const u32x2_t v0 = lds_read_tr16(vs + vrow * C::RB + 16 * v_chunk<HD>(vrow, c) + vhalf);
-    const u32x2_t v1 = lds_read_tr16(vs + (vrow + 16) * C::RB + 16 * v_chunk<HD>(vrow + 16, c) + vhalf);
-    const u32x4_t vf = u32x4_t{v0[0], v0[1], v1[0], v1[1]};
+  for (int b = 0; b < KT / 32; ++b) {
+    const int r0 = 32 * b + 4 * g + (l16 >> 2), r1 = r0 + 16;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) o[t][d] = mfma16x16x32<BF16>(vf, pf[t], o[t][d]);
+    for (int d = 0; d < HD / 16; ++d) {
+      const int c = 2 * d + ((l16 & 3) >> 1);
+      const u32x2_t v0 = lds_read_tr16(vs + r0 * C::RB + 16 * v_chunk<HD>(r0, c) + vhalf);
+      const u32x2_t v1 = lds_read_tr16(vs + r1 * C::RB + 16 * v_chunk<HD>(r1, c) + vhalf);
+      const u32x4_t vf = u32x4_t{v0[0], v0[1], v1[0], v1[1]};
+#pragma unroll
+      for (int t = 0; t < RT; ++t) w.o[t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t][d]);
+    }
   }
 
   if constexpr (EDGE) {
-    while (odd_rows) {
-      const int r = __builtin_ctz(odd_rows);
-      odd_rows &= odd_rows - 1;
+    while (odd) {
+      const int r = __builtin_ctzll(odd);
+      odd &= odd - 1;
       const uint16_t* vr = (const uint16_t*)((const uint8_t*)vh + (uint64_t)(uint32_t)slots[first + r] * a.v_row) + 4 * g;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         float p = 0.f;  // the row's weight of key r, from the lane that has it
+        uint32_t sees = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < KB; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if ((r >> 4) == h && (r & 3) == i) p = sc[t][h][i];
+#pragma unroll
+        for (int b = 0; b < KT / 32; ++b)
+          if ((r >> 5) == b) sees = (seen[t][b] >> (r & 31)) & 1;
         p = __shfl(p, l16 + 16 * ((r >> 2) & 3), 64);
-        const bool sees = (seen[t] >> r) & 1;
 #pragma unroll
         for (int d = 0; d < HD / 16; ++d)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             asm volatile("" ::: "memory");  // one element at a time: this path is rare, registers are not plenty
             const uint16_t x = vr[16 * d + i];
-            if (not_finite<BF16>(x) && sees) o[t][d][i] += p * act_to_f32<BF16>(x);
+            if (not_finite<BF16>(x) && sees) w.o[t][d][i] += p * act_to_f32<BF16>(x);
           }
       }
     }
   }
 }
 
-// ------------------------------------------------------------------------------ the kernel
+// 1 / sum; no key seen: 0; NaN stays
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f; }
+
+// ------------------------------------------------------------------------------ a workgroup's share
+// A piece of work: keys [key_lo, key_hi) of rows row0 .. of a tile.
+struct Piece {
+  Seq s;
+  int b, kvh, row0, rows;      // rows: of the sequence and cached head
+  int key_lo, key_hi;
+  bool whole, begins;          // all units of the tile; its first unit
+};
+
+// The piece at unit u of the share that ends at u_end; u moves past it.
+__device__ __forceinline__ Piece next_piece(const TreeArgs& a, int lane, int64_t& u, int64_t u_end) {
+  Piece p;
+  int64_t before;
+  p.b = find_sequence(a, lane, u, before);
+  p.s = sequence(a, p.b);
+  const int64_t in = u - before;
+  const int tile = (int)(in / p.s.units), u0 = (int)(in - (int64_t)tile * p.s.units);
+  const int u1 = (int)min((int64_t)p.s.units, u0 + (u_end - u));
+  u += u1 - u0;
+  p.kvh = tile / p.s.tiles;
+  p.row0 = (tile - p.kvh * p.s.tiles) * a.R;
+  p.rows = p.s.tokens * a.group;
+  p.key_lo = u0 * a.unit;
+  p.key_hi = (int)min((int64_t)p.s.len, (int64_t)u1 * a.unit);
+  if (!a.has_mask) {  // a chain's rows see no key past their last token
+    const int last = (int)divide((uint32_t)min(p.row0 + a.R, p.rows) - 1, a.by_group);
+    p.key_hi = (int)min((int64_t)p.key_hi, (int64_t)p.s.ctx + last + 1);
+  }
+  p.whole = u0 == 0 && u1 == p.s.units;
+  p.begins = u0 == 0;
+  return p;
+}
+
+// The slots of keys key0 .. + count - 1 of sequence b, -1 on no page; returns whether any is.
+__device__ __forceinline__ int find_slots(const TreeArgs& a, int b, int key0, int count, int* slots, int tid, int threads) {
+  int lost = 0;
+  for (int i = tid; i < count; i += threads) {
+    const uint32_t key = (uint32_t)(key0 + i), page = divide(key, a.by_page);
+    const int e = a.table[(int64_t)b * a.width + page];
+    const bool ok = e >= 0 && e < a.pages;
+    slots[i] = ok ? (int)((uint32_t)e * a.by_page.d + (key - page * a.by_page.d)) : -1;
+    lost |= !ok;
+  }
+  return lost;
+}
+
+// This workgroup's share of all units; false: none.  Shares in a row stand on one XCD (workgroups go
+// round the 8 XCDs), so that tiles of the same keys meet in its L2.
+__device__ __forceinline__ bool my_share(const TreeArgs& a, int lane, int64_t& me, int64_t& u, int64_t& u_end) {
+  const int64_t total = total_units(a, lane);
+  if (total == 0) return false;
+  const int64_t n = shares(a, total);
+  me = blockIdx.x;
+  if (me >= n) return false;
+  if ((n & 7) == 0) me = (me & 7) * (n >> 3) + (me >> 3);
+  u = share_begin(total, n, me);
+  u_end = share_begin(total, n, me + 1);
+  return true;
+}
+
+// ------------------------------------------------------------------------------ waves split the keys
+template <int HD, int RT>
+struct KeysLds {
+  static constexpr int NW = tree_key_waves(HD), R = 16 * RT, Pad = HD + 4;  // Pad: floats of a joining row
+  // the waves' stages, later their rows
+  static constexpr int Area = std::max(NW * 2 * Cfg<HD, 32>::Stage, NW * R * Pad * 4);
+  static constexpr int Total = Area + kSlots * 4 + NW * R * 8;  // slots, (base, sum) of each wave's rows
+};
+
 template <int HD, bool BF16, int RT>
-__global__ __launch_bounds__(64 * tree_waves(HD), RT == 4 || HD == 256 ? 1 : 2) void tree_kernel(const TreeArgs a) {
-  using C = Cfg<HD>;
-  constexpr int R = 16 * RT, NW = C::NW, UNIT = C::UNIT;
+__global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tree_keys_kernel(const TreeArgs a) {
+  using C = Cfg<HD, 32>;
+  using L = KeysLds<HD, RT>;
+  constexpr int R = L::R, NW = L::NW;
   extern __shared__ __align__(16) uint8_t lds[];
-  // stages of the waves (and after them the merge's rows), slots, row statistics of the waves
-  constexpr int kArea = std::max(NW * 2 * C::Stage, NW * R * C::Pad * 4);
-  int* slots = (int*)(lds + kArea);
-  float* stat = (float*)(lds + kArea + kSlots * 4);  // [NW][R][2]
+  int* slots = (int*)(lds + L::Area);
+  float* stat = (float*)(lds + L::Area + kSlots * 4);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-
-  const int64_t total = total_units<R, UNIT>(a, lane);
-  if (total == 0) return;
-  const int64_t n = shares(a, total);
-  // shares in a row on one XCD (workgroups go round the 8 XCDs): tiles of the same keys meet in its L2
-  int64_t me = blockIdx.x;
-  if (me >= n) return;
-  if ((n & 7) == 0) me = (me & 7) * (n >> 3) + (me >> 3);
-  int64_t u = share_begin(total, n, me);
-  const int64_t u_end = share_begin(total, n, me + 1);
+  int64_t me, u, u_end;
+  if (!my_share(a, lane, me, u, u_end)) return;
 
   while (u < u_end) {
-    int64_t before;
-    const int b = find_sequence<R, UNIT>(a, lane, u, before);
-    const Seq s = sequence<R, UNIT>(a, b);
-    const int64_t in = u - before;
-    const int tile = (int)(in / s.units), u0 = (int)(in - (int64_t)tile * s.units);
-    const int u1 = (int)min((int64_t)s.units, u0 + (u_end - u));
-    u += u1 - u0;
-    const int kvh = tile / s.tiles, row0 = (tile - kvh * s.tiles) * R, rows = s.tokens * a.group;
-
-    // this lane's row of each 16-row block, its token, and its query
-    int token[RT];
-    u32x4_t qf[RT][HD / 32];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int row = min(row0 + 16 * t + l16, rows - 1);
-      token[t] = (int)divide((uint32_t)row, a.by_group);
-      const int head = kvh * a.group + row - token[t] * a.group;
-      const uint16_t* qr = a.q + (int64_t)(s.q0 + token[t]) * a.q_t + (int64_t)head * a.q_h + 8 * g;
-#pragma unroll
-      for (int j = 0; j < HD / 32; ++j) qf[t][j] = (*(const u32x4_t*)(qr + 32 * j) & a.q_and) ^ a.q_xor;
-    }
-    const int key_lo = u0 * UNIT;
-    int key_hi = min(s.len, u1 * UNIT);
-    if (!a.has_mask) {  // a chain's rows see no key past their last token
-      const int last = (int)divide((uint32_t)min(row0 + R, rows) - 1, a.by_group);
-      key_hi = (int)min((int64_t)key_hi, (int64_t)s.ctx + last + 1);
-    }
-    const uint16_t* kh = a.k + (int64_t)kvh * a.k_h;
-    const uint16_t* vh = a.v + (int64_t)kvh * a.v_h;
-
-    f32x4_t o[RT][HD / 16];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      m[t] = kNone;
-      l[t] = 0.f;
-#pragma unroll
-      for (int d = 0; d < HD / 16; ++d) o[t][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    const Piece p = next_piece(a, lane, u, u_end);
+    const uint16_t* kh = a.k + (int64_t)p.kvh * a.k_h;
+    const uint16_t* vh = a.v + (int64_t)p.kvh * a.v_h;
+    Rows<HD, RT> w;
+    start_rows<HD, BF16, RT>(a, p.s, p.kvh, p.row0, p.rows, lane, w);
 
     uint8_t* mine = lds + wave * 2 * C::Stage;
-    for (int key0 = key_lo; key0 < key_hi; key0 += kSlots) {
-      const int count = min(kSlots, key_hi - key0);
-      int lost = 0;
-      __syncthreads();  // the slots (and the merge rows in the stages) have been read
-      for (int i = tid; i < count; i += 64 * NW) {
-        const uint32_t key = (uint32_t)(key0 + i), page = divide(key, a.by_page);
-        const int e = a.table[(int64_t)b * a.width + page];
-        const bool ok = e >= 0 && e < a.pages;
-        slots[i] = ok ? (int)((uint32_t)e * a.by_page.d + (key - page * a.by_page.d)) : -1;
-        lost |= !ok;
-      }
-      lost = __syncthreads_or(lost);
-
-      const int tiles = (count + kTreeKeys - 1) / kTreeKeys;
-      // everything this wave's loads below are counted against is then theirs alone
-      wave_wait<0>();
-      if (wave < tiles) load_tile<HD>(a, kh, vh, slots, wave * kTreeKeys, count, mine, lane);
+    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += kSlots) {
+      const int count = min(kSlots, p.key_hi - key0);
+      __syncthreads();  // the slots (and the joining rows in the stages) have been read
+      const int lost = __syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW));
+      const int tiles = (count + 31) / 32;
+      wave_wait<0>();  // from here on the loads in flight are the tiles'
+      if (wave < tiles) load_tile<HD, 32, 1>(a, kh, vh, slots, 32 * wave, count, mine, 0, lane);
       int st = 0;
       for (int j = wave; j < tiles; j += NW, st ^= 1) {
-        const int first = j * kTreeKeys;
+        const int first = 32 * j;
         if (j + NW < tiles) {
-          load_tile<HD>(a, kh, vh, slots, first + NW * kTreeKeys, count, mine + (st ^ 1) * C::Stage, lane);
+          load_tile<HD, 32, 1>(a, kh, vh, slots, first + 32 * NW, count, mine + (st ^ 1) * C::Stage, 0, lane);
           wave_wait<2 * C::Loads>();
         } else {
           wave_wait<0>();
         }
         uint8_t* stage = mine + st * C::Stage;
-        if (lost || first + kTreeKeys > count || key0 + first + kTreeKeys > s.ctx)
-          compute_tile<HD, BF16, RT, true>(a, s, slots, first, key0 + first, key0 + count, stage, vh, lane, qf, token, o,
-                                           m, l);
-        else
-          compute_tile<HD, BF16, RT, false>(a, s, slots, first, key0 + first, key0 + count, stage, vh, lane, qf, token,
-                                            o, m, l);
+        const int draft0 = key0 + first - p.s.ctx;
+        if (lost || first + 32 > count || draft0 + 32 > 0) {
+          const uint64_t keys = tile_keys<32>(slots, first, count, lane);
+          const uint64_t odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
+          __builtin_amdgcn_wave_barrier();
+          compute_tile<HD, BF16, RT, 32, true>(a, p.s, slots, first, draft0, keys, odd, stage, vh, lane, w);
+        } else {
+          compute_tile<HD, BF16, RT, 32, false>(a, p.s, slots, first, draft0, 0, 0, stage, vh, lane, w);
+        }
         // every read of this stage has returned before the next load into it
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
@@ -428,44 +525,42 @@ __global__ __launch_bounds__(64 * tree_waves(HD), RT == 4 || HD == 256 ? 1 : 2) 
     float* rowsum = (float*)lds;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      l[t] += __shfl_xor(l[t], 16, 64);
-      l[t] += __shfl_xor(l[t], 32, 64);
-      const int row = 16 * t + l16;
+      const float l = across<true>(w.l[t]);
+      const int row = wave * R + 16 * t + l16;
       if (g == 0) {
-        stat[(wave * R + row) * 2] = m[t];
-        stat[(wave * R + row) * 2 + 1] = l[t];
+        stat[row * 2] = w.m[t];
+        stat[row * 2 + 1] = l;
       }
 #pragma unroll
-      for (int d = 0; d < HD / 16; ++d) *(f32x4_t*)(rowsum + (wave * R + row) * C::Pad + 16 * d + 4 * g) = o[t][d];
+      for (int d = 0; d < HD / 16; ++d) *(f32x4_t*)(rowsum + row * L::Pad + 16 * d + 4 * g) = w.o[t][d];
     }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == s.units;
-    const int64_t part = 2 * me + (u0 == 0 ? 1 : 0);
+    const int64_t part = 2 * me + (p.begins ? 1 : 0);
     for (int e = tid; e < R * (HD / 8); e += 64 * NW) {
       const int row = e / (HD / 8), c = e % (HD / 8);
-      if (row0 + row >= rows) continue;
+      if (p.row0 + row >= p.rows) continue;
       float top = kNone;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) top = fmaxf(top, stat[(w * R + row) * 2]);
+      for (int i = 0; i < NW; ++i) top = fmaxf(top, stat[(i * R + row) * 2]);
       const float base = top == kNone ? 0.f : top;
       float sum = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float f = __builtin_amdgcn_exp2f(stat[(w * R + row) * 2] - base);
-        sum += f * stat[(w * R + row) * 2 + 1];
-        const f32x4_t y0 = *(const f32x4_t*)(rowsum + (w * R + row) * C::Pad + 8 * c);
-        const f32x4_t y1 = *(const f32x4_t*)(rowsum + (w * R + row) * C::Pad + 8 * c + 4);
+      for (int i = 0; i < NW; ++i) {
+        const float f = __builtin_amdgcn_exp2f(stat[(i * R + row) * 2] - base);
+        sum += f * stat[(i * R + row) * 2 + 1];
+        const f32x4_t y0 = *(const f32x4_t*)(rowsum + (i * R + row) * L::Pad + 8 * c);
+        const f32x4_t y1 = *(const f32x4_t*)(rowsum + (i * R + row) * L::Pad + 8 * c + 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[i] += f * y0[i];
-          y[4 + i] += f * y1[i];
+        for (int q = 0; q < 4; ++q) {
+          y[q] += f * y0[q];
+          y[4 + q] += f * y1[q];
         }
       }
-      if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
-        const int tk = (int)divide((uint32_t)(row0 + row), a.by_group);
-        const int head = kvh * a.group + row0 + row - tk * a.group;
-        *(u32x4_t*)(a.out + (int64_t)(s.q0 + tk) * a.o_t + (int64_t)head * a.o_h + 8 * c) =
+      if (p.whole) {
+        const float inv = inverse(sum);
+        const int tk = (int)divide((uint32_t)(p.row0 + row), a.by_group);
+        const int head = p.kvh * a.group + p.row0 + row - tk * a.group;
+        *(u32x4_t*)(a.out + (int64_t)(p.s.q0 + tk) * a.o_t + (int64_t)head * a.o_h + 8 * c) =
             u32x4_t{pack2<BF16>(y[0] * inv, y[1] * inv), pack2<BF16>(y[2] * inv, y[3] * inv),
                     pack2<BF16>(y[4] * inv, y[5] * inv), pack2<BF16>(y[6] * inv, y[7] * inv)};
       } else {
@@ -482,14 +577,99 @@ __global__ __launch_bounds__(64 * tree_waves(HD), RT == 4 || HD == 256 ? 1 : 2) 
   }
 }
 
+// ------------------------------------------------------------------------------ waves split the rows
+template <int HD, int NW>
+struct RowsLds {
+  static constexpr int KT = tree_row_keys(NW);
+  static constexpr int Area = 2 * Cfg<HD, KT>::Stage;
+  static constexpr int Total = Area + kSlots * 4 + NW * 8;  // slots, each wave's odd rows
+};
+
+template <int HD, bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a) {
+  constexpr int KT = RowsLds<HD, NW>::KT, RT = 2, R = 32 * NW;
+  using C = Cfg<HD, KT>;
+  extern __shared__ __align__(16) uint8_t lds[];
+  int* slots = (int*)(lds + RowsLds<HD, NW>::Area);
+  uint64_t* odd_of = (uint64_t*)(slots + kSlots);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  int64_t me, u, u_end;
+  if (!my_share(a, lane, me, u, u_end)) return;
+
+  while (u < u_end) {
+    const Piece p = next_piece(a, lane, u, u_end);
+    const uint16_t* kh = a.k + (int64_t)p.kvh * a.k_h;
+    const uint16_t* vh = a.v + (int64_t)p.kvh * a.v_h;
+    const int row0 = p.row0 + 16 * RT * wave;
+    Rows<HD, RT> w;
+    start_rows<HD, BF16, RT>(a, p.s, p.kvh, row0, p.rows, lane, w);
+    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += kSlots) {
+      const int count = min(kSlots, p.key_hi - key0);
+      __syncthreads();  // the slots and stages have been read
+      const int lost = __syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW));
+      const int tiles = (count + KT - 1) / KT;
+      wave_wait<0>();
+      load_tile<HD, KT, NW>(a, kh, vh, slots, 0, count, lds, wave, lane);
+      for (int j = 0; j < tiles; ++j) {
+        const int first = KT * j;
+        uint8_t* stage = lds + (j & 1) * C::Stage;
+        // this tile has landed for every wave, and every wave has read the one before it
+        stage_barrier<0>();
+        if (j + 1 < tiles)
+          load_tile<HD, KT, NW>(a, kh, vh, slots, first + KT, count, lds + ((j + 1) & 1) * C::Stage, wave, lane);
+        const int draft0 = key0 + first - p.s.ctx;
+        if (lost || first + KT > count || draft0 + KT > 0) {
+          const uint64_t keys = tile_keys<KT>(slots, first, count, lane);
+          const uint64_t mine = clean_values<HD, BF16, KT, NW>(stage, keys, wave, lane);
+          if (lane == 0) odd_of[wave] = mine;
+          __syncthreads();
+          uint64_t odd = 0;
+#pragma unroll
+          for (int i = 0; i < NW; ++i) odd |= odd_of[i];
+          compute_tile<HD, BF16, RT, KT, true>(a, p.s, slots, first, draft0, keys, odd, stage, vh, lane, w);
+        } else {
+          compute_tile<HD, BF16, RT, KT, false>(a, p.s, slots, first, draft0, 0, 0, stage, vh, lane, w);
+        }
+      }
+    }
+
+    const int64_t part = 2 * me + (p.begins ? 1 : 0);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int row = row0 + 16 * t + l16;
+      const float l = across<true>(w.l[t]);
+      if (row >= p.rows) continue;
+      if (p.whole) {
+        const float inv = inverse(l);
+        const int head = p.kvh * a.group + row - w.token[t] * a.group;
+        uint16_t* to = a.out + (int64_t)(p.s.q0 + w.token[t]) * a.o_t + (int64_t)head * a.o_h + 4 * g;
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d)
+          *(u32x2_t*)(to + 16 * d) = u32x2_t{pack2<BF16>(w.o[t][d][0] * inv, w.o[t][d][1] * inv),
+                                             pack2<BF16>(w.o[t][d][2] * inv, w.o[t][d][3] * inv)};
+      } else {
+        const int64_t at = part * R + row - p.row0;
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d) *(f32x4_t*)(a.part + at * HD + 16 * d + 4 * g) = w.o[t][d];
+        if (g == 0) {
+          a.part_ml[at * 2] = w.m[t];
+          a.part_ml[at * 2 + 1] = l;
+        }
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------ the join
 // One wave per query row and head: the parts of its tile, in key order.  HD / 64 elements a lane.
-template <int HD, bool BF16, int R>
+template <int HD, bool BF16>
 __global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
-  constexpr int UNIT = tree_unit(HD), E = HD / 64;
+  constexpr int E = HD / 64;
+  const int R = a.R;
   const int lane = threadIdx.x & 63;
   const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t total = total_units<R, UNIT>(a, lane);
+  const int64_t total = total_units(a, lane);
   if (total == 0 || id >= (int64_t)a.N * a.hq) return;
   const int64_t n = shares(a, total);
   const int tok = (int)(id / a.hq), head = (int)(id - (int64_t)tok * a.hq);
@@ -501,7 +681,7 @@ __global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
     int64_t own = 0;
     bool has = false;
     if (b0 + lane < a.B) {
-      const Seq s = sequence<R, UNIT>(a, b0 + lane);
+      const Seq s = sequence(a, b0 + lane);
       own = (int64_t)s.tiles * s.units * a.hkv;
       has = tok >= s.q0 && tok < s.q0 + s.tokens;
     }
@@ -514,7 +694,7 @@ __global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
     before += wave_sum(own);
   }
   if (b < 0) return;
-  const Seq s = sequence<R, UNIT>(a, b);
+  const Seq s = sequence(a, b);
   const int kvh = head / a.group, row = (tok - s.q0) * a.group + head - kvh * a.group;
   const int64_t u0 = before + ((int64_t)kvh * s.tiles + row / R) * s.units;
   const int64_t i0 = share_of(total, n, u0), i1 = share_of(total, n, u0 + s.units - 1);
@@ -532,36 +712,36 @@ __global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
     for (int e = 0; e < E; ++e) y[e] = y[e] * f0 + a.part[at * HD + lane * E + e] * f1;
     top = now;
   }
-  const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
+  const float inv = inverse(sum);
   uint16_t* to = a.out + (int64_t)tok * a.o_t + (int64_t)head * a.o_h + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e) to[e] = f32_to_act<BF16>(y[e] * inv);
 }
 
-template <int HD, bool BF16, int RT>
-hipError_t launch(const TreeArgs& a, hipStream_t stream) {
-  using C = Cfg<HD>;
-  constexpr int R = 16 * RT;
-  constexpr int lds = std::max(C::NW * 2 * C::Stage, C::NW * R * C::Pad * 4) + kSlots * 4 + C::NW * R * 8;
-  auto kern = tree_kernel<HD, BF16, RT>;
-  hipError_t e = raise_lds_limit((const void*)kern, lds);
+template <int HD, bool BF16>
+hipError_t launch(const TreeArgs& a, const TreePlan& pl, hipStream_t stream) {
+  const void* kern = nullptr;
+  int threads = 64 * pl.waves, lds = 0;
+  if (!pl.split_rows) {
+    threads = 64 * tree_key_waves(HD);
+    if (pl.rows == 16) kern = (const void*)tree_keys_kernel<HD, BF16, 1>, lds = KeysLds<HD, 1>::Total;
+    if constexpr (HD != 256)
+      if (pl.rows == 32) kern = (const void*)tree_keys_kernel<HD, BF16, 2>, lds = KeysLds<HD, 2>::Total;
+  } else if constexpr (HD != 256) {
+    if (pl.waves == 2) kern = (const void*)tree_rows_kernel<HD, BF16, 2>, lds = RowsLds<HD, 2>::Total;
+    if (pl.waves == 4) kern = (const void*)tree_rows_kernel<HD, BF16, 4>, lds = RowsLds<HD, 4>::Total;
+    if (pl.waves == 8) kern = (const void*)tree_rows_kernel<HD, BF16, 8>, lds = RowsLds<HD, 8>::Total;
+  }
+  if (!kern) return hipErrorInvalidValue;
+  hipError_t e = raise_lds_limit(kern, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)a.blocks), dim3(64 * C::NW), lds, stream, a);
-  e = hipGetLastError();
+  TreeArgs args = a;
+  void* argv[1] = {&args};
+  e = hipLaunchKernel(kern, dim3((unsigned)a.blocks), dim3((unsigned)threads), argv, (size_t)lds, stream);
   if (e != hipSuccess) return e;
   const int64_t waves = (int64_t)a.N * a.hq;
-  hipLaunchKernelGGL((tree_join_kernel<HD, BF16, R>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((tree_join_kernel<HD, BF16>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a);
   return hipGetLastError();
-}
-
-template <int HD, bool BF16>
-hipError_t launch_rows(const TreeArgs& a, int row_blocks, hipStream_t stream) {
-  if (row_blocks == 1) return launch<HD, BF16, 1>(a, stream);
-  if constexpr (HD != 256) {
-    if (row_blocks == 2) return launch<HD, BF16, 2>(a, stream);
-    if (row_blocks == 4) return launch<HD, BF16, 4>(a, stream);
-  }
-  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -571,7 +751,8 @@ hipError_t launch_tree(const TreeProblem& p, const TreePlan& pl, float scale, vo
   a.q = (const uint16_t*)p.q; a.k = (const uint16_t*)p.k; a.v = (const uint16_t*)p.v;
   a.table = p.table; a.context = p.context; a.starts = p.starts; a.mask = p.mask; a.out = (uint16_t*)p.out;
   a.part = (float*)workspace;
-  a.part_ml = a.part + pl.blocks * 2 * 16 * pl.row_blocks * p.d;
+  a.part_ml = a.part + pl.blocks * 2 * pl.rows * p.d;
+  a.R = pl.rows; a.unit = pl.unit;
   a.q_t = p.q_t; a.q_h = p.q_h; a.k_h = p.k_h; a.v_h = p.v_h;
   a.o_t = p.o_t; a.o_h = p.o_h;
   a.k_row = (uint32_t)(2 * p.k_t); a.v_row = (uint32_t)(2 * p.v_t);
@@ -583,9 +764,9 @@ hipError_t launch_tree(const TreeProblem& p, const TreePlan& pl, float scale, vo
   a.q_xor = scale < 0.f ? 0x80008000u : 0u;
   const bool bf16 = p.act == WQ_BF16;
   switch (p.d) {
-    case 64: return bf16 ? launch_rows<64, true>(a, pl.row_blocks, stream) : launch_rows<64, false>(a, pl.row_blocks, stream);
-    case 128: return bf16 ? launch_rows<128, true>(a, pl.row_blocks, stream) : launch_rows<128, false>(a, pl.row_blocks, stream);
-    default: return bf16 ? launch_rows<256, true>(a, pl.row_blocks, stream) : launch_rows<256, false>(a, pl.row_blocks, stream);
+    case 64: return bf16 ? launch<64, true>(a, pl, stream) : launch<64, false>(a, pl, stream);
+    case 128: return bf16 ? launch<128, true>(a, pl, stream) : launch<128, false>(a, pl, stream);
+    default: return bf16 ? launch<256, true>(a, pl, stream) : launch<256, false>(a, pl, stream);
   }
 }
 
