@@ -6,19 +6,40 @@
 //
 // Tokens of one adapter need not stand together, and nothing is sorted: the token rows are
 // cut into windows of 16 or 64, and a work item is one (window, distinct adapter of it)
-// pair.  Every wave finds the window's distinct adapters with one load of 64 indices and
-// ballots; the item's product is taken for whole 16-row blocks of the window and only the
-// rows of its adapter are stored, so a row never depends on its neighbours.  A sort would
-// read an adapter once for all its tokens where the pairs read it once per window, but costs
-// a dependent launch; adapters are a few hundred KB and stay in the L2s.
+// pair.  The item's product is taken for whole 16-row blocks of the window and only the rows
+// of its adapter are stored, so a row never depends on its neighbours.  Up to kLoraSmallM
+// tokens, windows are 16 rows and every workgroup finds its window's distinct adapters by
+// itself, with one load of 16 indices and ballots: a launch less.  Beyond, windows are 64 rows,
+// a first kernel lists the items, and the workgroups of the others walk that list.
+//
+// Both products move far more memory than they multiply; what bounds them is how the reads
+// meet the caches and channels:
+//  * workgroups side by side on the chip take different columns of the same rows (second
+//    product) or start at different k (first product).  Rows are a power of two apart in most
+//    models; walked down in step, all of a chip's reads would meet on a few channels.
+//  * each XCD takes a run of neighbouring items, so that its L2 holds the adapters of those only;
+//  * operands go to LDS first (direct loads, each wave into its own), in rows of adjacent lanes, and
+//    from there into the matrix cores' layout.  Loaded from memory in that layout, where lanes
+//    that follow each other hold different rows, every lane is an access of its own: 389 us
+//    instead of 125 us without the loads of B, for 16384 tokens x 8192 columns at rank 64.
 #include <algorithm>
 
 #include "serve_device.h"
 #include "serve_kernels.h"
 #include "serve_tile.h"
+#include "wq_pipeline.h"
 
 namespace wq {
 namespace {
+
+// A window (its first token), an adapter (-1: rows without one), its rank and scale, and the rows
+// that have it.
+struct Item {
+  int64_t w0;
+  uint64_t rows;
+  int32_t key, rank;
+  float scale;
+};
 
 struct LoraArgs {
   const uint16_t* x1;
@@ -30,8 +51,10 @@ struct LoraArgs {
   const uint16_t* x3;
   uint16_t* out;
   float* h;               // [splits][m][r]
-  int64_t m, n, sx, s3, so;
-  int32_t k, r, L, splits, kchunk, slots;
+  Item* items;            // 64-row windows: the lists, and the lengths
+  int32_t* count;
+  int64_t m, n, sx, s3, so, windows;
+  int32_t k, r, L, splits, kchunk, slots, cols, col_blocks, rank_blocks;
 };
 
 // The adapter of this lane's row of the window at w0 (rows past m and lanes past the window:
@@ -43,119 +66,211 @@ __device__ __forceinline__ int lane_key(const LoraArgs& p, int64_t w0, int lane)
   return (uint32_t)i < (uint32_t)p.L ? i : -1;
 }
 
-__device__ __forceinline__ int adapter_rank(const LoraArgs& p, int i) {
-  return p.ranks ? min(max(p.ranks[i], 0), p.r) : p.r;
+__device__ __forceinline__ Item make_item(const LoraArgs& p, int64_t w0, int key, uint64_t rows) {
+  Item it{w0, rows, key, 0, 1.f};
+  if (key >= 0) {
+    it.rank = p.ranks ? min(max(p.ranks[key], 0), p.r) : p.r;
+    if (p.scale) it.scale = p.scale[key];
+  }
+  return it;
+}
+
+// The items of 64-row windows.  The first item of window w is items[w]; the others of the windows of
+// workgroup i of this kernel stand from items[windows + its first row] on, count[i] of them, in any
+// order (items do not depend on each other).
+__global__ __launch_bounds__(256) void lora_items_kernel(const LoraArgs p) {
+  __shared__ int32_t more;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x == 0) more = 0;
+  __syncthreads();
+  const int64_t share = (p.windows + kLoraLists - 1) / kLoraLists, lo = blockIdx.x * share;
+  const int64_t hi = min(p.windows, lo + share);
+  for (int64_t w = lo + wave; w < hi; w += 4) {
+    const int mine = lane_key<64>(p, w * 64, lane);
+    uint64_t left = __ballot(mine >= -1);
+    for (int s = 0; left; ++s) {
+      const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+      const uint64_t rows = __ballot(mine == key);
+      left &= ~rows;
+      if (lane == 0) p.items[s == 0 ? w : p.windows + lo * 64 + atomicAdd(&more, 1)] = make_item(p, w * 64, key, rows);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) p.count[blockIdx.x] = more;
+}
+
+// Calls body(item, part) for this workgroup's items, `parts` workgroups to an item, parts fastest; each
+// XCD has an eighth of the row of units.  16-row windows: one unit to a workgroup, windows x slots x
+// parts of them, and a workgroup takes every slots-th distinct adapter of its window.  64-row
+// windows: the workgroups walk the list.
+template <int W, typename Body>
+__device__ __forceinline__ void for_items(const LoraArgs& p, int parts, const Body& body) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (W == 16) {
+    const uint32_t u = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    const int part = u % parts, slot = u / parts % p.slots;
+    const int64_t w0 = (int64_t)(u / parts / p.slots) * W;
+    const int mine = lane_key<W>(p, w0, lane);  // windows past the last have no rows
+    uint64_t left = __ballot(mine >= -1);
+    for (int s = 0; left; ++s) {
+      const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+      const uint64_t rows = __ballot(mine == key);
+      left &= ~rows;
+      if (s % p.slots == slot) body(make_item(p, w0, key, rows), part);
+    }
+  } else {
+    static_assert(kLoraLists == 64, "a lane for each list");
+    const int own = p.count[lane];
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += t;
+    }
+    const int64_t total = (p.windows + __shfl(upto, 63, 64)) * parts, eighth = (total + 7) / 8;
+    const int64_t share = (p.windows + kLoraLists - 1) / kLoraLists;
+    const int64_t end = min(total, ((blockIdx.x & 7) + 1) * eighth);
+    for (int64_t u = (blockIdx.x & 7) * eighth + (blockIdx.x >> 3); u < end; u += gridDim.x >> 3) {
+      int64_t i = u / parts;
+      if (i >= p.windows) {  // an item of one of the lists
+        const int e = (int)(i - p.windows), at = __builtin_ctzll(__ballot(upto > e));
+        i = p.windows + at * share * 64 + e - __shfl(upto - own, at, 64);
+      }
+      body(p.items[i], (int)(u % parts));
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------- h = x1 A^T
-// One item's h for up to kLoraRankTiles 16-rank tiles from rank r0 and the workgroup's k
-// chunk.  MT 16-row blocks from row w0 + 16 * m0.  The four waves take 64-k steps in turn
-// (two 16x16x32 MFMAs: rows of x1 against rows of A_i, both k-contiguous, 16 bytes a lane
-// straight from global memory) and their sums meet in LDS, in wave order.
-template <bool BF16, int MT>
-__device__ __forceinline__ void shrink_item(const LoraArgs& p, float* red, int64_t w0, int m0, int key, uint64_t rows,
+// A wave's stage is a step of 64 k: 16 MT rows of x1, then 16 NT rows of A_i, 128 bytes each, with
+// the chunks of a row in row_slot's places.
+template <int MT, int NT>
+struct ShrinkStage {
+  static constexpr int X = MT * 2048, Bytes = (MT + NT) * 2048, Loads = 2 * (MT + NT);
+};
+
+// One item's h for NT 16-rank tiles from rank r0 and the workgroup's k chunk.  MT 16-row blocks
+// from row w0 + 16 * m0.  The NW waves take 64-k steps in turn, two 16x16x32 MFMAs each (rows of
+// x1 against rows of A_i), the next step on its way meanwhile, and their sums meet in LDS, in
+// wave order.
+template <bool BF16, int MT, int NT, int NW>
+__device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int64_t w0, int m0, int key, uint64_t rows,
                                             int r0, int kb, int ke, float* h) {
+  using S = ShrinkStage<MT, NT>;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  const int nt = min(kLoraRankTiles, (p.r - r0 + 15) / 16);
-  const uint16_t* xr[MT];
-  const uint16_t* ar[kLoraRankTiles];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) xr[t] = p.x1 + min(w0 + 16 * (m0 + t) + l16, p.m - 1) * p.sx + 8 * g;
-#pragma unroll
-  for (int j = 0; j < kLoraRankTiles; ++j)
-    ar[j] = p.a + ((int64_t)key * p.r + min(r0 + 16 * j + l16, p.r - 1)) * p.k + 8 * g;
-  f32x4_t acc[MT][kLoraRankTiles];
+  f32x4_t acc[MT][NT];
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int j = 0; j < kLoraRankTiles; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < NT; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  int k0 = kb + 64 * wave;
-#pragma unroll 2
-  for (; k0 + 64 <= ke; k0 += 256) {
-    u32x4_t xf[MT][2], af[kLoraRankTiles][2];
+  // one load takes 8 rows; rows past m or r read the last one, and their sums are not stored
+  const uint16_t* src[S::Loads];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t) xf[t][s] = *(const u32x4_t*)(xr[t] + k0 + 32 * s);
-#pragma unroll
-      for (int j = 0; j < kLoraRankTiles; ++j)
-        if (j < nt) af[j][s] = *(const u32x4_t*)(ar[j] + k0 + 32 * s);
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < kLoraRankTiles; ++j)
-        if (j < nt)
-#pragma unroll
-          for (int t = 0; t < MT; ++t) acc[t][j] = mfma16x16x32<BF16>(xf[t][s], af[j][s], acc[t][j]);
+  for (int i = 0; i < S::Loads; ++i) {
+    const int row = 8 * i + (lane >> 3);  // of the stage
+    const int c = 8 * row_slot<128>(row, lane & 7);
+    if (i < 2 * MT) src[i] = p.x1 + min(w0 + 16 * m0 + row, p.m - 1) * p.sx + c;
+    else src[i] = p.a + ((int64_t)key * p.r + min(r0 + row - 16 * MT, p.r - 1)) * p.k + c;
   }
-  if (k0 < ke) {  // the k tail: 8-k pieces past ke are zeros on both sides
+  uint8_t* mine = lds + wave * 2 * S::Bytes;
+  const int full = (ke - kb) / 64;  // whole steps; the waves take them in turn from step `turn` on
+  const int turn = (int)((w0 >> 4) % 1024) * NW;
+  auto load = [&](int i, uint8_t* stage) {
+    const int k0 = kb + 64 * (int)((uint32_t)(i + turn) % (uint32_t)full);
+#pragma unroll
+    for (int l = 0; l < S::Loads; ++l) dma16_global(src[l] + k0, stage + 1024 * l);
+  };
+  auto multiply = [&](const uint8_t* stage) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const bool in = k0 + 32 * s + 8 * g < ke;
       u32x4_t xf[MT];
+      const int slot = 16 * row_slot<128>(l16, 4 * s + g);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) xf[t] = in ? *(const u32x4_t*)(xr[t] + k0 + 32 * s) : u32x4_t{0, 0, 0, 0};
+      for (int t = 0; t < MT; ++t) xf[t] = *(const u32x4_t*)(stage + (16 * t + l16) * 128 + slot);
 #pragma unroll
-      for (int j = 0; j < kLoraRankTiles; ++j)
-        if (j < nt) {
-          const u32x4_t af = in ? *(const u32x4_t*)(ar[j] + k0 + 32 * s) : u32x4_t{0, 0, 0, 0};
+      for (int j = 0; j < NT; ++j) {
+        const u32x4_t af = *(const u32x4_t*)(stage + S::X + (16 * j + l16) * 128 + slot);
 #pragma unroll
-          for (int t = 0; t < MT; ++t) acc[t][j] = mfma16x16x32<BF16>(xf[t], af, acc[t][j]);
-        }
-    }
-  }
-  // block t of row blocks: element i of a lane is row 4 g + i, rank l16
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kLoraRankTiles; ++j)
-      if (j < nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[(wave * 16 + 4 * g + i) * (16 * kLoraRankTiles) + 16 * j + l16] = acc[t][j][i];
-    __syncthreads();
-    const int c = tid & 63;
-    if (c < 16 * nt && r0 + c < p.r) {
-      for (int row = tid >> 6; row < 16; row += 4) {
-        const int wr = 16 * (m0 + t) + row;
-        if (!((rows >> wr) & 1)) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) v += red[(w * 16 + row) * (16 * kLoraRankTiles) + c];
-        h[(w0 + wr) * p.r + r0 + c] = v;
+        for (int t = 0; t < MT; ++t) acc[t][j] = mfma16x16x32<BF16>(xf[t], af, acc[t][j]);
       }
     }
+  };
+  __syncthreads();  // the LDS has been read
+  wave_wait<0>();
+  int st = 0;
+  if (wave < full) load(wave, mine);
+  for (int i = wave; i < full; i += NW, st ^= 1) {
+    if (i + NW < full) {
+      load(i + NW, mine + (st ^ 1) * S::Bytes);
+      wave_wait<S::Loads>();
+    } else {
+      wave_wait<0>();
+    }
+    multiply(mine + st * S::Bytes);
+    // every read of this stage has returned before the next load into it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+  const int k0 = kb + 64 * full;
+  if (k0 < ke && wave == full % NW) {  // the k tail: 8-k pieces past ke are zeros on both sides
+#pragma unroll
+    for (int l = 0; l < S::Loads; ++l) {
+      const int row = 8 * l + (lane >> 3);
+      u32x4_t v = u32x4_t{0, 0, 0, 0};
+      if (k0 + 8 * row_slot<128>(row, lane & 7) < ke) v = *(const u32x4_t*)(src[l] + k0);
+      *(u32x4_t*)(mine + 1024 * l + 16 * lane) = v;
+    }
+    __builtin_amdgcn_wave_barrier();
+    multiply(mine);
+  }
+  // block t of row blocks: element i of a lane is row 4 g + i, rank l16
+  float* red = (float*)lds;
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[(wave * 16 * MT + 16 * t + 4 * g + i) * (16 * NT) + 16 * j + l16] = acc[t][j][i];
+  __syncthreads();
+  for (int e = tid; e < 256 * MT * NT; e += 64 * NW) {
+    const int row = e / (16 * NT), c = e % (16 * NT), wr = 16 * m0 + row;
+    if (r0 + c >= p.r || !((rows >> wr) & 1)) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += red[w * (256 * MT * NT) + e];
+    h[(w0 + wr) * p.r + r0 + c] = v;
   }
 }
 
-// Grid x: windows, y: slots x blocks of kLoraRankTiles rank tiles, z: k splits.
-template <bool BF16, int W>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs p) {
-  __shared__ float red[4 * 16 * 16 * kLoraRankTiles];
-  const int lane = threadIdx.x & 63;
-  const int64_t w0 = (int64_t)blockIdx.x * W;
-  const int slot = blockIdx.y % p.slots, r0 = (blockIdx.y / p.slots) * 16 * kLoraRankTiles;
-  const int kb = blockIdx.z * p.kchunk, ke = min(p.k, kb + p.kchunk);
-  float* h = p.h + (int64_t)blockIdx.z * p.m * p.r;
-  const int mine = lane_key<W>(p, w0, lane);
-  uint64_t left = __ballot(mine >= 0);
-  for (int s = 0; left; ++s) {
-    const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-    const uint64_t rows = __ballot(mine == key);
-    left &= ~rows;
-    if (s % p.slots != slot || r0 >= adapter_rank(p, key)) continue;
+constexpr int kShrinkWaves = 4;
+template <int W, int NT>
+constexpr int shrink_lds() {
+  constexpr int MT = W == 16 ? 1 : 4;
+  return kShrinkWaves * std::max(2 * ShrinkStage<MT, NT>::Bytes, 1024 * MT * NT);
+}
+
+// Parts of an item: blocks of NT rank tiles x k splits, splits fastest.
+template <bool BF16, int W, int NT>
+__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const LoraArgs p) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int NW = kShrinkWaves;
+  for_items<W>(p, p.splits * p.rank_blocks, [&](const Item& it, int part) {
+    const int split = part % p.splits, r0 = part / p.splits * (16 * NT);
+    if (r0 >= it.rank) return;
+    const int kb = split * p.kchunk, ke = min(p.k, kb + p.kchunk);
+    float* h = p.h + (int64_t)split * p.m * p.r;
     if constexpr (W == 16) {
-      shrink_item<BF16, 1>(p, red, w0, 0, key, rows, r0, kb, ke, h);
+      shrink_item<BF16, 1, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
     } else {
       // rows inside one 16-row block (single tokens, the ends of prompts) read that block only
-      const int lo = __builtin_ctzll(rows) >> 4, hi = (63 - __builtin_clzll(rows)) >> 4;
-      if (lo == hi) shrink_item<BF16, 1>(p, red, w0, lo, key, rows, r0, kb, ke, h);
-      else shrink_item<BF16, 4>(p, red, w0, 0, key, rows, r0, kb, ke, h);
+      const int lo = __builtin_ctzll(it.rows) >> 4, hi = (63 - __builtin_clzll(it.rows)) >> 4;
+      if (lo == hi) shrink_item<BF16, 1, NT, NW>(p, lds, it.w0, lo, it.key, it.rows, r0, kb, ke, h);
+      else shrink_item<BF16, 4, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
     }
-  }
+  });
 }
 
 // ------------------------------------------------------------------------- out = x3 + h B^T
@@ -178,45 +293,98 @@ __device__ __forceinline__ uint32_t split_hi_lo(float v) {  // hi in bits 0-15, 
   return (uint32_t)hi | ((uint32_t)lo << 16);
 }
 
-// Grid x: windows, y: blocks of NC * 4 columns (NC per wave), z: slots.  Dynamic LDS: W rows of
-// hp = (r rounded up to 16) + 4 packed values, then W row factors.
-template <bool BF16, int W, int NC>
+// B in LDS: 32 columns of CH 16-byte chunks (8 ranks each), chunk c of column n in slot
+// c ^ column_turn(n): the 16 columns that one read takes (4 neighbours of every 8) then stand in 16
+// different places of the 256 bytes that a bank cycle covers.
+__device__ __forceinline__ int column_turn(int n) { return ((n >> 1) & 1) | (((n >> 3) & 3) << 1); }
+
+// Parts of an item: blocks of p.cols columns.  A wave takes the window's rows (MT 16-row blocks) x 32
+// columns at a time, and the ranks in blocks of up to 8 CH.  Dynamic LDS: two stages of B for
+// each wave, W rows of hp = (r rounded up to 16) + 4 packed values, W row factors.
+template <bool BF16, int W, int CH>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs p) {
-  extern __shared__ uint32_t lds[];
-  constexpr int MT = W / 16, NP = NC / 32;
+  extern __shared__ __align__(16) uint8_t stages[];
+  constexpr int MT = W / 16, Stage = 32 * CH * 16, Loads = Stage / 1024, RB = 8 * CH;  // RB: ranks of a stage
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  const int64_t w0 = (int64_t)blockIdx.x * W;
-  const int64_t n0 = (int64_t)blockIdx.y * (4 * NC) + wave * NC;
   const int r16 = (p.r + 15) & ~15, hp = r16 + 4;
+  uint32_t* lds = (uint32_t*)(stages + 8 * Stage);
   float* factor = (float*)(lds + W * hp);
-  const int mine = lane_key<W>(p, w0, lane);
-  uint64_t left = __ballot(mine >= -1);
-  for (int s = 0; left; ++s) {
-    const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-    const uint64_t rows = __ballot(mine == key);
-    left &= ~rows;
-    if (s % p.slots != (int)blockIdx.z) continue;
-    const int rank = key < 0 ? 0 : adapter_rank(p, key);
-    const int nk = (rank + 15) / 16;
-    if (rank == 0 && p.x3 == p.out) continue;  // nothing to add in place
+  uint8_t* mine = stages + wave * 2 * Stage;
+  for_items<W>(p, p.col_blocks, [&](const Item& it, int part) {
+    const int key = it.key;
+    const uint64_t rows = it.rows;
+    const int64_t w0 = it.w0;
+    const int64_t n1 = min(p.n, ((int64_t)part + 1) * p.cols);
+    int64_t nc = (int64_t)part * p.cols + wave * 32;
+    const int rank = it.rank;
+    if (rank == 0 && p.x3 == p.out) return;  // nothing to add in place
+    const int nk = (rank + 15) / 16, steps = (rank + RB - 1) / RB;
+
+    // Loads take any row or column of the tensors where theirs are past the end (what comes of it is not
+    // stored, or is cleared below): without a condition they all go out at once.
+    const uint16_t* bk = p.b + (int64_t)max(key, 0) * p.n * p.r;
+    u32x4_t x[MT];
+    auto load_x = [&](int64_t nc) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        x[t] = u32x4_t{0, 0, 0, 0};
+        if (p.x3 && ((rows >> (16 * t)) & 0xffff))
+          x[t] = *(const u32x4_t*)(p.x3 + min(w0 + 16 * t + l16, p.m - 1) * p.s3 + min(nc + 8 * g, p.n - 8));
+      }
+    };
+    auto load_b = [&](int64_t nc, int r0, uint8_t* stage) {  // ranks r0 .. + RB - 1
+#pragma unroll
+      for (int i = 0; i < Loads; ++i) {
+        const int e = 64 * i + lane, n = e / CH, c = (e % CH) ^ (column_turn(n) & (CH - 1));
+        dma16_global(bk + min(nc + n, p.n - 1) * p.r + min(r0 + 8 * c, p.r - 8), stage + 1024 * i);
+      }
+    };
+    const bool busy = nc < n1;
+    if (busy) {  // on their way while h is made ready
+      load_x(nc);
+      if (rank) load_b(nc, 0, mine);
+    }
 
     if (rank) {  // h of the adapter's rows: splits added in order, scaled, split into hi + lo
       __syncthreads();
-      constexpr int TPR = 256 / W;  // threads of a row
-      const int row = tid / TPR, c0 = tid % TPR;
+      constexpr int TPR = 256 / W;  // threads of a row, four ranks each at a time
+      const int row = tid / TPR, first = 4 * (tid % TPR);
       const bool have = (rows >> row) & 1;
-      const float sc = p.scale ? p.scale[key] : 1.f;
+      const float sc = it.scale;
+      const float* hr = p.h + (w0 + row) * p.r;
+      const int64_t step = p.m * p.r;
       float big = 0.f;
-      for (int c = c0; c < 16 * nk; c += TPR) {
-        float v = 0.f;
-        if (have && c < rank) {
-          const float* hr = p.h + (w0 + row) * p.r + c;
-          for (int z = 0; z < p.splits; ++z) v += hr[(int64_t)z * p.m * p.r];
-          v *= sc;
+      auto keep = [&](f32x4_t v, int c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = have && c + i < rank ? v[i] * sc : 0.f;
+          if (__builtin_isfinite(v[i])) big = fmaxf(big, fabsf(v[i]));  // infinities and NaN stay what they are
         }
-        if (__builtin_isfinite(v)) big = fmaxf(big, fabsf(v));  // infinities and NaN stay what they are
-        lds[row * hp + c] = __float_as_uint(v);
+        *(f32x4_t*)(lds + row * hp + c) = v;
+      };
+      if (p.splits == 1) {
+        for (int c = first; c < 16 * nk; c += 16 * TPR) {  // four loads in flight
+          f32x4_t t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (have && c + 4 * TPR * i < rank) t[i] = *(const f32x4_t*)(hr + c + 4 * TPR * i);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + 4 * TPR * i < 16 * nk) keep(t[i], c + 4 * TPR * i);
+        }
+      } else {
+        for (int c = first; c < 16 * nk; c += 4 * TPR) {
+          f32x4_t t[kLoraSplits], v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+          if (have && c < rank) {  // all splits in flight
+#pragma unroll
+            for (int z = 0; z < kLoraSplits; ++z) t[z] = *(const f32x4_t*)(hr + min(z, p.splits - 1) * step + c);
+#pragma unroll
+            for (int z = 0; z < kLoraSplits; ++z)
+              if (z < p.splits) v += t[z];
+          }
+          keep(v, c);
+        }
       }
 #pragma unroll
       for (int o = 1; o < TPR; o <<= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
@@ -224,94 +392,117 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs p) {
       int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 : 0;
       e = min(max(e, -126), 126);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      if (c0 == 0) factor[row] = __uint_as_float((uint32_t)(127 + e) << 23);
-      for (int c = c0; c < 16 * nk; c += TPR)
-        lds[row * hp + c] = split_hi_lo<BF16>(__uint_as_float(lds[row * hp + c]) * down);
+      if (first == 0) factor[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+      for (int c = first; c < 16 * nk; c += 4 * TPR) {
+        const f32x4_t v = *(const f32x4_t*)(lds + row * hp + c);
+        *(u32x4_t*)(lds + row * hp + c) = u32x4_t{split_hi_lo<BF16>(v[0] * down), split_hi_lo<BF16>(v[1] * down),
+                                                  split_hi_lo<BF16>(v[2] * down), split_hi_lo<BF16>(v[3] * down)};
+      }
       __syncthreads();
     }
+    if (!busy) return;
 
-    f32x4_t acc[NP][2][MT];
-#pragma unroll
-    for (int q = 0; q < NP; ++q)
+    f32x4_t acc[2][MT];
+    int st = 0;
+#pragma unroll 1
+    for (; nc < n1; nc += kLoraCols) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[q][e][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* bk = p.b + (int64_t)max(key, 0) * p.n * p.r;
-    for (int j = 0; j < nk; ++j) {
-      const int c = 16 * j + 8 * (g & 1);  // this lane's 8 ranks
-      u32x4_t hf[MT];
+        for (int t = 0; t < MT; ++t) acc[e][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < steps; ++s, st ^= 1) {
+        const bool last = s + 1 == steps;
+        if (!last || nc + kLoraCols < n1) {
+          load_b(last ? nc + kLoraCols : nc, last ? 0 : RB * (s + 1), mine + (st ^ 1) * Stage);
+          wave_wait<Loads>();
+        } else {
+          wave_wait<0>();
+        }
+        const uint8_t* stage = mine + st * Stage;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const u32x4_t* src = (const u32x4_t*)(lds + (16 * t + l16) * hp + c);
-        const u32x4_t u = src[0], v = src[1];
-        const uint32_t sel = g < 2 ? 0x05040100u : 0x07060302u;  // the hi or the lo halves
-        hf[t] = u32x4_t{__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel),
-                        __builtin_amdgcn_perm(v[1], v[0], sel), __builtin_amdgcn_perm(v[3], v[2], sel)};
-      }
+        for (int j = 0; j < CH / 2; ++j) {
+          const int c = RB * s + 16 * j + 8 * (g & 1);  // this lane's 8 ranks
+          if (RB * s + 16 * j >= rank) break;
+          u32x4_t hf[MT], bf[2];
 #pragma unroll
-      for (int q = 0; q < NP; ++q)
+          for (int t = 0; t < MT; ++t) {
+            const u32x4_t* src = (const u32x4_t*)(lds + (16 * t + l16) * hp + c);
+            const u32x4_t u = src[0], v = src[1];
+            const uint32_t sel = g < 2 ? 0x05040100u : 0x07060302u;  // the hi or the lo halves
+            hf[t] = u32x4_t{__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel),
+                            __builtin_amdgcn_perm(v[1], v[0], sel), __builtin_amdgcn_perm(v[3], v[2], sel)};
+          }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t n = n0 + 32 * q + 8 * (l16 >> 2) + 4 * e + (l16 & 3);
-          u32x4_t bf = u32x4_t{0, 0, 0, 0};
-          if (n < p.n && c < rank) {
-            bf = *(const u32x4_t*)(bk + n * p.r + c);
-            if (c + 8 > rank) {  // columns past the rank hold anything
+          for (int e = 0; e < 2; ++e) {
+            const int n = 8 * (l16 >> 2) + 4 * e + (l16 & 3);
+            bf[e] = *(const u32x4_t*)(stage + 16 * (n * CH + ((2 * j + (g & 1)) ^ (column_turn(n) & (CH - 1)))));
+          }
+          if (RB * s + 16 * j + 16 > rank) {  // columns past the rank hold anything
 #pragma unroll
-              for (int d = 0; d < 4; ++d)
-                bf[d] &= (c + 2 * d < rank ? 0x0000ffffu : 0u) | (c + 2 * d + 1 < rank ? 0xffff0000u : 0u);
+            for (int d = 0; d < 4; ++d) {
+              const uint32_t keep = (c + 2 * d < rank ? 0x0000ffffu : 0u) | (c + 2 * d + 1 < rank ? 0xffff0000u : 0u);
+              bf[0][d] &= keep;
+              bf[1][d] &= keep;
             }
           }
 #pragma unroll
-          for (int t = 0; t < MT; ++t) acc[q][e][t] = mfma16x16x32<BF16>(bf, hf[t], acc[q][e][t]);
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[e][t] = mfma16x16x32<BF16>(bf[e], hf[t], acc[e][t]);
         }
-    }
+        // every read of this stage has returned before the next load into it
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+      u32x4_t o[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int wr = 16 * t + l16;
-      if (!((rows >> wr) & 1)) continue;
-      const int64_t row = w0 + wr;
-      const float f = rank ? factor[wr] : 0.f;
-#pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        const int64_t n = n0 + 32 * q + 8 * g;
-        if (n >= p.n) continue;
-        u32x4_t x = u32x4_t{0, 0, 0, 0};
-        if (p.x3) x = *(const u32x4_t*)(p.x3 + row * p.s3 + n);
+      for (int t = 0; t < MT; ++t) {
+        o[t] = x[t];
         if (rank) {
-          u32x4_t o;
+          const float f = factor[16 * t + l16];
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            const f32x4_t& y = acc[q][d >> 1][t];
-            const float lo = act_to_f32<BF16>((uint16_t)x[d]) + f * y[2 * (d & 1)];
-            const float hi = act_to_f32<BF16>((uint16_t)(x[d] >> 16)) + f * y[2 * (d & 1) + 1];
-            o[d] = pack2<BF16>(lo, hi);
+            const f32x4_t& y = acc[d >> 1][t];
+            const float lo = act_to_f32<BF16>((uint16_t)o[t][d]) + f * y[2 * (d & 1)];
+            const float hi = act_to_f32<BF16>((uint16_t)(o[t][d] >> 16)) + f * y[2 * (d & 1) + 1];
+            o[t][d] = pack2<BF16>(lo, hi);
           }
-          x = o;
         }
-        *(u32x4_t*)(p.out + row * p.so + n) = x;
+      }
+      if (nc + kLoraCols < n1) load_x(nc + kLoraCols);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int wr = 16 * t + l16;
+        if (((rows >> wr) & 1) && nc + 8 * g < n1) *(u32x4_t*)(p.out + (w0 + wr) * p.so + nc + 8 * g) = o[t];
       }
     }
+  });
+}
+
+// NT: 16-rank tiles of the first product's workgroups, and half the 16-byte chunks of a column of
+// the second's stages.
+template <bool BF16, int W, int NT>
+hipError_t launch(const LoraArgs& a, const LoraPlan& pl, hipStream_t stream) {
+  hipError_t e;
+  if constexpr (W == 64) {
+    hipLaunchKernelGGL(lora_items_kernel, dim3(kLoraLists), dim3(256), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
+  auto shrink = lora_shrink_kernel<BF16, W, NT>;
+  if ((e = raise_lds_limit((const void*)shrink, shrink_lds<W, NT>())) != hipSuccess) return e;
+  hipLaunchKernelGGL(shrink, dim3((unsigned)pl.shrink_blocks), dim3(64 * kShrinkWaves), (shrink_lds<W, NT>()), stream, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const size_t lds = 8 * (32 * 2 * NT * 16) + (size_t)W * (((a.r + 15) & ~15) + 4 + 1) * 4;
+  auto expand = lora_expand_kernel<BF16, W, 2 * NT>;
+  if ((e = raise_lds_limit((const void*)expand, (int)lds)) != hipSuccess) return e;
+  hipLaunchKernelGGL(expand, dim3((unsigned)pl.expand_blocks), dim3(256), lds, stream, a);
+  return hipGetLastError();
 }
 
 template <bool BF16, int W>
-hipError_t launch(const LoraArgs& a, const LoraPlan& pl, hipStream_t stream) {
-  const int rank_blocks = (a.r + 16 * kLoraRankTiles - 1) / (16 * kLoraRankTiles);
-  hipLaunchKernelGGL((lora_shrink_kernel<BF16, W>),
-                     dim3((unsigned)pl.windows, (unsigned)(pl.slots * rank_blocks), (unsigned)pl.splits), dim3(256), 0,
-                     stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  constexpr int NC = W == 16 ? 32 : 64;
-  const size_t lds = (size_t)W * (((a.r + 15) & ~15) + 4 + 1) * 4;
-  auto kern = lora_expand_kernel<BF16, W, NC>;
-  e = raise_lds_limit((const void*)kern, (int)lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)pl.windows, (unsigned)((a.n + 4 * NC - 1) / (4 * NC)), (unsigned)pl.slots),
-                     dim3(256), lds, stream, a);
-  return hipGetLastError();
+hipError_t launch_ranks(const LoraArgs& a, const LoraPlan& pl, hipStream_t stream) {
+  if (pl.rank_tiles == 1) return launch<BF16, W, 1>(a, pl, stream);
+  if (pl.rank_tiles == 2) return launch<BF16, W, 2>(a, pl, stream);
+  return launch<BF16, W, 4>(a, pl, stream);
 }
 
 }  // namespace
@@ -320,12 +511,16 @@ hipError_t launch_lora(const LoraProblem& p, const LoraPlan& pl, void* workspace
   LoraArgs a{};
   a.x1 = (const uint16_t*)p.x1; a.a = (const uint16_t*)p.a; a.b = (const uint16_t*)p.b;
   a.indices = p.indices; a.scale = p.scale; a.ranks = p.ranks;
-  a.x3 = (const uint16_t*)p.x3; a.out = (uint16_t*)p.out; a.h = (float*)workspace;
+  a.x3 = (const uint16_t*)p.x3; a.out = (uint16_t*)p.out; a.h = (float*)((char*)workspace + pl.list_bytes);
+  a.count = (int32_t*)workspace;
+  a.items = (Item*)((char*)workspace + 4 * kLoraLists);
   a.m = p.m; a.n = p.n; a.sx = p.sx; a.s3 = p.s3; a.so = p.so;
-  a.k = p.k; a.r = p.r; a.L = (int32_t)p.L; a.splits = pl.splits; a.kchunk = pl.kchunk; a.slots = pl.slots;
+  a.k = p.k; a.r = p.r; a.L = (int32_t)p.L; a.splits = pl.splits; a.kchunk = pl.kchunk; a.slots = pl.slots; a.cols = pl.cols;
+  a.windows = pl.windows; a.col_blocks = pl.col_blocks; a.rank_blocks = pl.rank_blocks;
+  static_assert(sizeof(Item) == kLoraItemBytes, "the plan's size of the list");
   const bool bf16 = p.act == WQ_BF16;
-  if (pl.window == 16) return bf16 ? launch<true, 16>(a, pl, stream) : launch<false, 16>(a, pl, stream);
-  return bf16 ? launch<true, 64>(a, pl, stream) : launch<false, 64>(a, pl, stream);
+  if (pl.window == 16) return bf16 ? launch_ranks<true, 16>(a, pl, stream) : launch_ranks<false, 16>(a, pl, stream);
+  return bf16 ? launch_ranks<true, 64>(a, pl, stream) : launch_ranks<false, 64>(a, pl, stream);
 }
 
 }  // namespace wq

@@ -18,18 +18,37 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 LoraPlan plan_lora(const LoraProblem& p) {
   LoraPlan pl;
+  if (p.m == 0) return pl;
   pl.window = p.m <= kLoraSmallM ? 16 : 64;
   pl.windows = ceil_div(p.m, pl.window);
-  // Side-by-side work items of a window: its rows may each have an adapter of their own.
+  // Side-by-side work items of a 16-row window, whose rows may each have an adapter of their own:
+  // all of them where there are few windows, otherwise 4 (most workgroups of more would find nothing).
   const int64_t distinct = std::min<int64_t>({p.L + 1, p.m, pl.window});
-  pl.slots = (int)std::max<int64_t>(1, std::min<int64_t>(distinct, p.m <= 64 ? 16 : 4));
-  const int rank_blocks = (int)ceil_div(p.r, 16 * kLoraRankTiles);
-  const int64_t want = 2 * kCUs / std::max<int64_t>(1, pl.windows * rank_blocks);
-  int64_t splits = std::min<int64_t>({want, 16, ceil_div(p.k, 256)});
-  splits = std::max<int64_t>(1, splits);
-  pl.kchunk = (int)(ceil_div(ceil_div(p.k, splits), 64) * 64);
+  if (pl.window == 16) pl.slots = (int)std::min<int64_t>(distinct, p.m <= 64 ? 16 : 4);
+  pl.rank_tiles = p.r <= 16 ? 1 : p.r <= 32 ? 2 : kLoraRankTiles;
+  pl.rank_blocks = (int)ceil_div(p.r, 16 * pl.rank_tiles);
+  // k splits, a power of two (a split then stays on its XCDs), while workgroups are few
+  const int64_t most = ceil_div(p.k, 256);
+  while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && pl.windows * pl.rank_blocks * pl.splits < 2 * kCUs)
+    pl.splits *= 2;
+  pl.kchunk = (int)(ceil_div(ceil_div(p.k, pl.splits), 64) * 64);
   pl.splits = (int)ceil_div(p.k, pl.kchunk);
-  pl.workspace = p.m == 0 ? 0 : align256((int64_t)pl.splits * p.m * p.r * 4);
+  // second product: workgroups of whole rounds of columns, as many as reside at once if a larger
+  // window has about two adapters
+  const int64_t rounds = ceil_div(p.n, kLoraCols);
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(rounds, 4 * kCUs / (pl.windows * (p.m <= 64 ? pl.slots : 2))));
+  pl.cols = (int)(ceil_div(rounds, blocks) * kLoraCols);
+  if (pl.window == 64) pl.cols = (int)std::min<int64_t>(rounds, 4) * kLoraCols;
+  pl.col_blocks = (int)ceil_div(p.n, pl.cols);
+  if (pl.window == 16) {
+    pl.shrink_blocks = ceil_div(pl.windows * pl.slots * pl.rank_blocks * pl.splits, 8) * 8;
+    pl.expand_blocks = ceil_div(pl.windows * pl.slots * pl.col_blocks, 8) * 8;
+  } else {  // as many as reside at once walk the list; both multiples of 8
+    pl.shrink_blocks = kCUs;
+    pl.expand_blocks = 2 * kCUs;
+    pl.list_bytes = align256(4 * kLoraLists + (p.m + 2 * pl.windows) * kLoraItemBytes);
+  }
+  pl.workspace = align256(pl.list_bytes + (int64_t)pl.splits * p.m * p.r * 4);
   return pl;
 }
 

@@ -34,12 +34,18 @@ struct LoraProblem {
 };
 
 struct LoraPlan {
-  int window = 16;       // token rows of a work item (16 or 64)
+  int window = 16;         // token rows of a work item (16 or 64)
   int64_t windows = 0;
-  int slots = 1;         // work items per window that run side by side
-  int splits = 1;        // k splits of the first product
-  int kchunk = 0;        // k per split, a multiple of 64
-  int64_t workspace = 0; // fp32 partials of x1 @ a^T, [splits][m][r]
+  int slots = 1;           // 16-row windows: work items of one that run side by side
+  int splits = 1;          // k splits of the first product
+  int kchunk = 0;          // k per split, a multiple of 64
+  int rank_tiles = 4;      // 16-rank tiles of a workgroup of the first product, and blocks of them
+  int rank_blocks = 1;
+  int cols = 128;          // columns of a workgroup of the second product, and blocks of them
+  int col_blocks = 1;
+  int64_t shrink_blocks = 0, expand_blocks = 0;  // workgroups of the two products
+  int64_t list_bytes = 0;  // 64-row windows: the list of work items and its length
+  int64_t workspace = 0;   // the list, then fp32 partials of x1 @ a^T, [splits][m][r]
 };
 
 struct RopeProblem {

@@ -7,7 +7,11 @@ namespace wq {
 
 // ---- adapters
 constexpr int64_t kLoraSmallM = 1024;  // up to here a window is 16 token rows, beyond 64
-constexpr int kLoraRankTiles = 4;      // 16-rank tiles that one workgroup of the first product computes
+constexpr int kLoraRankTiles = 4;      // most 16-rank tiles of one workgroup of the first product
+constexpr int kLoraCols = 128;         // columns of one round of the second product's workgroups
+constexpr int kLoraSplits = 8;         // most k splits of the first product
+constexpr int kLoraItemBytes = 32;      // a work item in the lists of the 64-row windows, and the number of lists
+constexpr int kLoraLists = 64;
 
 // ---- tree attention
 constexpr int tree_key_waves(int d) { return d == 256 ? 2 : 4; }   // waves that split the keys, 32 to a tile
