@@ -153,7 +153,7 @@ struct ShrinkStage {
 // from row w0 + 16 * m0.  The NW waves take 64-k steps in turn, two 16x16x32 MFMAs each (rows of
 // x1 against rows of A_i), the next step on its way meanwhile, and their sums meet in LDS, in
 // wave order.
-template <bool BF16, int MT, int NT, int NW>
+template <bool BF16, int W, int MT, int NT, int NW>
 __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int64_t w0, int m0, int key, uint64_t rows,
                                             int r0, int kb, int ke, float* h) {
   using S = ShrinkStage<MT, NT>;
@@ -176,7 +176,7 @@ __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int
   }
   uint8_t* mine = lds + wave * 2 * S::Bytes;
   const int full = (ke - kb) / 64;  // whole steps; the waves take them in turn from step `turn` on
-  const int turn = (int)((w0 >> 4) % 1024) * NW;
+  const int turn = (int)(w0 / W % 1024) * NW;
   auto load = [&](int i, uint8_t* stage) {
     const int k0 = kb + 64 * (int)((uint32_t)(i + turn) % (uint32_t)full);
 #pragma unroll
@@ -248,8 +248,7 @@ __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int
 constexpr int kShrinkWaves = 4;
 template <int W, int NT>
 constexpr int shrink_lds() {
-  constexpr int MT = W == 16 ? 1 : 4;
-  return kShrinkWaves * std::max(2 * ShrinkStage<MT, NT>::Bytes, 1024 * MT * NT);
+  return kShrinkWaves * std::max(2 * ShrinkStage<W / 16, NT>::Bytes, 1024 * (W / 16) * NT);
 }
 
 // Parts of an item: blocks of NT rank tiles x k splits, splits fastest.
@@ -263,12 +262,12 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const Lo
     const int kb = split * p.kchunk, ke = min(p.k, kb + p.kchunk);
     float* h = p.h + (int64_t)split * p.m * p.r;
     if constexpr (W == 16) {
-      shrink_item<BF16, 1, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
+      shrink_item<BF16, W, 1, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
     } else {
       // rows inside one 16-row block (single tokens, the ends of prompts) read that block only
       const int lo = __builtin_ctzll(it.rows) >> 4, hi = (63 - __builtin_clzll(it.rows)) >> 4;
-      if (lo == hi) shrink_item<BF16, 1, NT, NW>(p, lds, it.w0, lo, it.key, it.rows, r0, kb, ke, h);
-      else shrink_item<BF16, 4, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
+      if (lo == hi) shrink_item<BF16, W, 1, NT, NW>(p, lds, it.w0, lo, it.key, it.rows, r0, kb, ke, h);
+      else shrink_item<BF16, W, 4, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
     }
   });
 }
@@ -296,19 +295,23 @@ __device__ __forceinline__ uint32_t split_hi_lo(float v) {  // hi in bits 0-15, 
 // B in LDS: 32 columns of CH 16-byte chunks (8 ranks each), chunk c of column n in slot
 // c ^ column_turn(n): the 16 columns that one read takes (4 neighbours of every 8) then stand in 16
 // different places of the 256 bytes that a bank cycle covers.
+constexpr int kSumRow = 36;  // floats of a row of 32 sums: rows 16 bytes apart in the banks
 __device__ __forceinline__ int column_turn(int n) { return ((n >> 1) & 1) | (((n >> 3) & 3) << 1); }
 
 // Parts of an item: blocks of p.cols columns.  A wave takes the window's rows (MT 16-row blocks) x 32
-// columns at a time, and the ranks in blocks of up to 8 CH.  Dynamic LDS: two stages of B for
-// each wave, W rows of hp = (r rounded up to 16) + 4 packed values, W row factors.
+// columns at a time, and the ranks in blocks of up to 8 CH.  Its sums go through LDS, 16 rows at a time,
+// so that four adjacent lanes read x3 and write the output in 64 bytes of a row.  Dynamic LDS: for
+// each wave two stages of B and 16 rows of sums, then W rows of hp = (r rounded up to 16) + 4
+// packed values, then W row factors.
 template <bool BF16, int W, int CH>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs p) {
+__global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expand_kernel(const LoraArgs p) {
   extern __shared__ __align__(16) uint8_t stages[];
   constexpr int MT = W / 16, Stage = 32 * CH * 16, Loads = Stage / 1024, RB = 8 * CH;  // RB: ranks of a stage
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
   const int r16 = (p.r + 15) & ~15, hp = r16 + 4;
-  uint32_t* lds = (uint32_t*)(stages + 8 * Stage);
+  float* sums = (float*)(stages + 8 * Stage) + wave * (16 * kSumRow);
+  uint32_t* lds = (uint32_t*)(stages + 8 * Stage + 4 * 16 * kSumRow * 4);
   float* factor = (float*)(lds + W * hp);
   uint8_t* mine = stages + wave * 2 * Stage;
   for_items<W>(p, p.col_blocks, [&](const Item& it, int part) {
@@ -324,13 +327,14 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs p) {
     // Loads take any row or column of the tensors where theirs are past the end (what comes of it is not
     // stored, or is cleared below): without a condition they all go out at once.
     const uint16_t* bk = p.b + (int64_t)max(key, 0) * p.n * p.r;
+    const int row4 = lane >> 2, col4 = 8 * (lane & 3);  // of each 16 rows x 32 columns of x3 and output
     u32x4_t x[MT];
     auto load_x = [&](int64_t nc) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         x[t] = u32x4_t{0, 0, 0, 0};
         if (p.x3 && ((rows >> (16 * t)) & 0xffff))
-          x[t] = *(const u32x4_t*)(p.x3 + min(w0 + 16 * t + l16, p.m - 1) * p.s3 + min(nc + 8 * g, p.n - 8));
+          x[t] = *(const u32x4_t*)(p.x3 + min(w0 + 16 * t + row4, p.m - 1) * p.s3 + min(nc + col4, p.n - 8));
       }
     };
     auto load_b = [&](int64_t nc, int r0, uint8_t* stage) {  // ranks r0 .. + RB - 1
@@ -458,21 +462,28 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs p) {
       for (int t = 0; t < MT; ++t) {
         o[t] = x[t];
         if (rank) {
-          const float f = factor[16 * t + l16];
+          // lane l16's row, columns 8 g .. + 7
+          *(f32x4_t*)(sums + l16 * kSumRow + 8 * g) = acc[0][t];
+          *(f32x4_t*)(sums + l16 * kSumRow + 8 * g + 4) = acc[1][t];
+          __builtin_amdgcn_wave_barrier();
+          const f32x4_t y0 = *(const f32x4_t*)(sums + row4 * kSumRow + col4);
+          const f32x4_t y1 = *(const f32x4_t*)(sums + row4 * kSumRow + col4 + 4);
+          const float f = factor[16 * t + row4];
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            const f32x4_t& y = acc[d >> 1][t];
+            const f32x4_t& y = d < 2 ? y0 : y1;
             const float lo = act_to_f32<BF16>((uint16_t)o[t][d]) + f * y[2 * (d & 1)];
             const float hi = act_to_f32<BF16>((uint16_t)(o[t][d] >> 16)) + f * y[2 * (d & 1) + 1];
             o[t][d] = pack2<BF16>(lo, hi);
           }
+          __builtin_amdgcn_wave_barrier();
         }
       }
       if (nc + kLoraCols < n1) load_x(nc + kLoraCols);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const int wr = 16 * t + l16;
-        if (((rows >> wr) & 1) && nc + 8 * g < n1) *(u32x4_t*)(p.out + (w0 + wr) * p.so + nc + 8 * g) = o[t];
+        const int wr = 16 * t + row4;
+        if (((rows >> wr) & 1) && nc + col4 < n1) *(u32x4_t*)(p.out + (w0 + wr) * p.so + nc + col4) = o[t];
       }
     }
   });
@@ -491,7 +502,7 @@ hipError_t launch(const LoraArgs& a, const LoraPlan& pl, hipStream_t stream) {
   if ((e = raise_lds_limit((const void*)shrink, shrink_lds<W, NT>())) != hipSuccess) return e;
   hipLaunchKernelGGL(shrink, dim3((unsigned)pl.shrink_blocks), dim3(64 * kShrinkWaves), (shrink_lds<W, NT>()), stream, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const size_t lds = 8 * (32 * 2 * NT * 16) + (size_t)W * (((a.r + 15) & ~15) + 4 + 1) * 4;
+  const size_t lds = 8 * (32 * 2 * NT * 16) + 4 * 16 * kSumRow * 4 + (size_t)W * (((a.r + 15) & ~15) + 4 + 1) * 4;
   auto expand = lora_expand_kernel<BF16, W, 2 * NT>;
   if ((e = raise_lds_limit((const void*)expand, (int)lds)) != hipSuccess) return e;
   hipLaunchKernelGGL(expand, dim3((unsigned)pl.expand_blocks), dim3(256), lds, stream, a);
