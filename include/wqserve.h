@@ -104,7 +104,8 @@ int wq_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq
  * the caches.  A token that sees no key gives zeros.  What a token does not see has no part in
  * its result, NaN and infinities included.
  *
- *   q             required; WQ_F16 or WQ_BF16; rows (N, hq, d); d in {64, 128, 256}.
+ *   q             required; WQ_F16 or WQ_BF16; rows (N, hq, d); d in {64, 128, 256}; N at most
+ *                 2^24 and N * hq at most 2^30.
  *   k_cache       required; q's dtype; rows (S, hkv, d); S a multiple of page_size, at most
  *                 2^31-1; its row stride at most 2^30; hq a multiple of hkv.
  *   v_cache       required; q's dtype; rows (S, hkv, d), like k_cache.

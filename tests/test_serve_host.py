@@ -200,10 +200,10 @@ def test_tree_accepts(wqlib):
     both = [20 * 16, 2, 128]
     assert tree(wqlib, k_cache=D(both, BF, strides=[512, 128, 1]), v_cache=D(both, BF, strides=[512, 128, 1]))[0] == OK
     assert tree(wqlib, q=D([7, 8, 128], BF, strides=[2048, 128, 1]))[0] == OK
-    # a workspace of some megabytes whatever the lengths
+    # a workspace of some megabytes whatever the lengths, and notes of a few bytes a query token
     for kw in (dict(N=1 << 24, B=65535, width=127, page=1 << 20, pages=2047), dict(N=64, B=1, width=1 << 17)):
         st, size = tree(wqlib, **tree_args(**kw))
-        assert st == OK and size <= 66 << 20
+        assert st == OK and size <= (66 << 20) + 2 * kw["N"]
 
 
 def test_tree_refuses(wqlib):
@@ -225,7 +225,7 @@ def test_tree_refuses(wqlib):
             assert tree(wqlib, **{name: D(shape, BF, strides=[1024, 128, 2])}) == INVALID, name
         else:
             assert tree(wqlib, **{name: D(shape, I32, ptr=0x10002)}) == INVALID, name
-    for bad in (dict(d=96), dict(d=512), dict(hq=7), dict(hkv=3), dict(hkv=0), dict(hq=2, hkv=4), dict(N=(1 << 24) + 1),
+    for bad in (dict(d=96), dict(d=512), dict(hq=7), dict(hkv=3), dict(hkv=0), dict(hq=2, hkv=4), dict(N=(1 << 24) + 1), dict(N=1 << 22, hq=512),
                 dict(B=65536), dict(width=1 << 27), dict(words=(1 << 20) + 1)):
         assert tree(wqlib, **tree_args(**bad)) == INVALID, bad
     for page in (0, -16, 7, (1 << 20) + 1):

@@ -72,11 +72,12 @@ TreePlan plan_tree(const TreeProblem& p) {
     per_cu = 8 / pl.waves;
   }
   // tiles: each sequence with tokens has ceil(T_b * group / rows) for each cached head
-  const int64_t tiles = (p.N * p.group / pl.rows + std::min(p.N, p.B)) * p.hkv;
+  pl.tiles = (p.N * p.group / pl.rows + std::min(p.N, p.B)) * p.hkv;
   const int64_t units = std::max<int64_t>(1, ceil_div((int64_t)p.width * p.page, pl.unit));
-  pl.blocks = std::min<int64_t>(kCUs * per_cu, tiles * units);
+  pl.blocks = std::min<int64_t>(kCUs * per_cu, pl.tiles * units);
+  pl.notes_bytes = align256((pl.tiles + 1) * kTreeCutBytes);
   // two partial tiles for each workgroup: outputs, then (base, sum) of each row
-  pl.workspace = align256(pl.blocks * 2 * pl.rows * (int64_t)(p.d + 2) * 4);
+  pl.workspace = align256(pl.notes_bytes + pl.blocks * 2 * pl.rows * (int64_t)(p.d + 2) * 4);
   return pl;
 }
 

@@ -90,7 +90,9 @@ struct TreePlan {
   int rows = 16;            // of a tile: tokens x query heads of a cached head
   int unit = 128;           // keys, the unit of the work that workgroups share
   int64_t blocks = 0;       // workgroups (an upper bound of the shares)
-  int64_t workspace = 0;
+  int64_t tiles = 0;        // an upper bound of the tiles
+  int64_t notes_bytes = 0;  // the tiles' notes
+  int64_t workspace = 0;    // the notes, then two partial tiles for each workgroup
 };
 
 int validate_lora(const wq_tensor* x1, const wq_tensor* a, const wq_tensor* b, const wq_tensor* indices,

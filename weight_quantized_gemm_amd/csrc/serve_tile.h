@@ -15,6 +15,7 @@ constexpr int kLoraLists = 64;
 
 // ---- tree attention
 constexpr int tree_key_waves(int d) { return d == 256 ? 2 : 4; }   // waves that split the keys, 32 to a tile
+constexpr int kTreeCutBytes = 32;      // what is noted of a tile for the join
 constexpr int tree_row_keys(int waves) { return waves == 2 ? 32 : 64; }  // keys of a tile whose rows the waves split
 
 }  // namespace wq

@@ -8,8 +8,9 @@
 // tile, key).  Each workgroup takes an equal share of that row, wherever it begins and ends:
 // ragged lengths, few long sequences and many short ones load the chip alike, without knowing a
 // length on the host.  A tile that one workgroup holds whole is written by it; one that is cut
-// leaves partial results (output, maximum, sum) that a second kernel joins in key order.  A
-// workgroup has at most two such parts: its first and its last.
+// leaves partial results (output, base, sum) that a second kernel joins in key order.  A
+// workgroup has at most two such parts, its first and its last; the one that holds a tile's first
+// keys notes what is to be joined.
 //
 // Two kernels, by the rows of the average sequence (plan_tree):
 //   keys: up to 32 rows, bound by memory.  The waves of a workgroup split the keys; each streams
@@ -43,13 +44,21 @@
 namespace wq {
 namespace {
 
+// What the join needs of a tile: its parts are the second part of workgroup `first` and the first
+// parts of the next parts - 1.  parts 0: the tile was not cut.
+struct Cut {
+  int32_t parts, first, q0, kvh, row0, rows, pad[2];
+};
+
 struct TreeArgs {
   const uint16_t *q, *k, *v;
   const int32_t *table, *context, *starts;
   const uint32_t* mask;
   uint16_t* out;
   float* part;        // partial outputs [2 * blocks][R][d]
-  float* part_ml;     // their (maximum, sum) [2 * blocks][R][2]
+  float* part_ml;     // their (base, sum) [2 * blocks][R][2]
+  Cut* cuts;          // of each tile, in the row's order
+  int32_t* tiles;     // how many there are
   int64_t q_t, q_h, k_h, v_h, o_t, o_h;
   uint32_t k_row, v_row;  // bytes from one slot to the next
   int64_t pages;
@@ -90,41 +99,59 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
+__device__ __forceinline__ int64_t wave_upto(int64_t v, int lane) {  // of lanes 0 .. lane
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t t = __shfl_up(v, o, 64);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+__device__ __forceinline__ int64_t units_of(const TreeArgs& a, const Seq& s) { return (int64_t)s.tiles * s.units * a.hkv; }
+
+// 64 sequences as a wave sees them: lane l has sequence b0 + l, and the units and tiles up to and with
+// it among the 64.
+struct Sight {
+  Seq mine;
+  int64_t units = 0, tiles = 0;
+};
+
+__device__ __forceinline__ Sight see(const TreeArgs& a, int lane, int b0) {
+  Sight c;
+  if (b0 + lane < a.B) c.mine = sequence(a, b0 + lane);
+  c.units = wave_upto(units_of(a, c.mine), lane);
+  c.tiles = wave_upto((int64_t)c.mine.tiles * a.hkv, lane);
+  return c;
+}
 
 __device__ __forceinline__ int64_t total_units(const TreeArgs& a, int lane) {
   int64_t sum = 0;
-  for (int b = lane; b < a.B; b += 64) {
-    const Seq s = sequence(a, b);
-    sum += (int64_t)s.tiles * s.units * a.hkv;
-  }
+  for (int b = lane; b < a.B; b += 64) sum += units_of(a, sequence(a, b));
   return wave_sum(sum);
 }
 
-// The sequence that holds unit u (u < total), and the number of units before it.
-__device__ __forceinline__ int find_sequence(const TreeArgs& a, int lane, int64_t u, int64_t& before) {
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int64_t own = 0;
-    if (b0 + lane < a.B) {
-      const Seq s = sequence(a, b0 + lane);
-      own = (int64_t)s.tiles * s.units * a.hkv;
-    }
-    int64_t upto = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t t = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += t;
-    }
-    const uint64_t past = __ballot(base + upto > u);
+// The sequence that holds unit u (u < total), and the units and tiles before it.
+__device__ __forceinline__ int find_sequence(const TreeArgs& a, int lane, int64_t u, Seq& s, int64_t& before,
+                                             int64_t& tiles_before) {
+  int64_t base = 0, tiles = 0;
+  for (int b0 = 0;; b0 += 64) {
+    const Sight c = see(a, lane, b0);
+    const uint64_t past = __ballot(base + c.units > u);
     if (past) {
       const int at = __builtin_ctzll(past);
-      before = base + __shfl(upto - own, at, 64);
+      before = base + __shfl(c.units - units_of(a, c.mine), at, 64);
+      tiles_before = tiles + __shfl(c.tiles - (int64_t)c.mine.tiles * a.hkv, at, 64);
+      s.q0 = __builtin_amdgcn_readlane(c.mine.q0, at);
+      s.tokens = __builtin_amdgcn_readlane(c.mine.tokens, at);
+      s.ctx = __builtin_amdgcn_readlane(c.mine.ctx, at);
+      s.len = __builtin_amdgcn_readlane(c.mine.len, at);
+      s.tiles = __builtin_amdgcn_readlane(c.mine.tiles, at);
+      s.units = __builtin_amdgcn_readlane(c.mine.units, at);
       return b0 + at;
     }
-    base += __shfl(upto, 63, 64);
+    base += __shfl(c.units, 63, 64);
+    tiles += __shfl(c.tiles, 63, 64);
   }
-  before = base;
-  return -1;
 }
 
 // Workgroups that share `total` units, and the first unit of share i.
@@ -406,14 +433,14 @@ struct Piece {
   int b, kvh, row0, rows;      // rows: of the sequence and cached head
   int key_lo, key_hi;
   bool whole, begins;          // all units of the tile; its first unit
+  int64_t tile_end, tile_id;   // the unit past the tile; its place among all tiles
 };
 
 // The piece at unit u of the share that ends at u_end; u moves past it.
 __device__ __forceinline__ Piece next_piece(const TreeArgs& a, int lane, int64_t& u, int64_t u_end) {
   Piece p;
-  int64_t before;
-  p.b = find_sequence(a, lane, u, before);
-  p.s = sequence(a, p.b);
+  int64_t before, tiles_before;
+  p.b = find_sequence(a, lane, u, p.s, before, tiles_before);
   const int64_t in = u - before;
   const int tile = (int)(in / p.s.units), u0 = (int)(in - (int64_t)tile * p.s.units);
   const int u1 = (int)min((int64_t)p.s.units, u0 + (u_end - u));
@@ -427,6 +454,8 @@ __device__ __forceinline__ Piece next_piece(const TreeArgs& a, int lane, int64_t
     const int last = (int)divide((uint32_t)min(p.row0 + a.R, p.rows) - 1, a.by_group);
     p.key_hi = (int)min((int64_t)p.key_hi, (int64_t)p.s.ctx + last + 1);
   }
+  p.tile_end = before + (int64_t)(tile + 1) * p.s.units;
+  p.tile_id = tiles_before + tile;
   p.whole = u0 == 0 && u1 == p.s.units;
   p.begins = u0 == 0;
   return p;
@@ -445,18 +474,26 @@ __device__ __forceinline__ int find_slots(const TreeArgs& a, int b, int key0, in
   return lost;
 }
 
-// This workgroup's share of all units; false: none.  Shares in a row stand on one XCD (workgroups go
-// round the 8 XCDs), so that tiles of the same keys meet in its L2.
-__device__ __forceinline__ bool my_share(const TreeArgs& a, int lane, int64_t& me, int64_t& u, int64_t& u_end) {
-  const int64_t total = total_units(a, lane);
-  if (total == 0) return false;
+// This workgroup's share of all `total` units; false: none.  Shares in a row stand on one XCD
+// (workgroups go round the 8 XCDs), so that tiles of the same keys meet in its L2.
+__device__ __forceinline__ bool my_share(const TreeArgs& a, int lane, int64_t& total, int64_t& me, int64_t& u, int64_t& u_end) {
+  total = total_units(a, lane);
   const int64_t n = shares(a, total);
   me = blockIdx.x;
+  if (n == 0 && me == 0 && threadIdx.x == 0) *a.tiles = 0;
   if (me >= n) return false;
   if ((n & 7) == 0) me = (me & 7) * (n >> 3) + (me >> 3);
   u = share_begin(total, n, me);
   u_end = share_begin(total, n, me + 1);
   return true;
+}
+
+// Notes the tile of a piece with its first keys.  The last tile's place is the number of tiles, less 1.
+__device__ __forceinline__ void note_tile(const TreeArgs& a, int64_t total, int64_t me, const Piece& p) {
+  if (threadIdx.x != 0 || !p.begins) return;
+  const int64_t last = share_of(total, shares(a, total), p.tile_end - 1);
+  a.cuts[p.tile_id] = Cut{p.whole ? 0 : (int)(last - me) + 1, (int)me, p.s.q0, p.kvh, p.row0, p.rows, {0, 0}};
+  if (p.tile_end == total) *a.tiles = (int)(p.tile_id + 1);
 }
 
 // ------------------------------------------------------------------------------ waves split the keys
@@ -478,11 +515,12 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
   float* stat = (float*)(lds + L::Area + kSlots * 4);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  int64_t me, u, u_end;
-  if (!my_share(a, lane, me, u, u_end)) return;
+  int64_t total, me, u, u_end;
+  if (!my_share(a, lane, total, me, u, u_end)) return;
 
   while (u < u_end) {
     const Piece p = next_piece(a, lane, u, u_end);
+    note_tile(a, total, me, p);
     const uint16_t* kh = a.k + (int64_t)p.kvh * a.k_h;
     const uint16_t* vh = a.v + (int64_t)p.kvh * a.v_h;
     Rows<HD, RT> w;
@@ -594,11 +632,12 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
   uint64_t* odd_of = (uint64_t*)(slots + kSlots);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  int64_t me, u, u_end;
-  if (!my_share(a, lane, me, u, u_end)) return;
+  int64_t total, me, u, u_end;
+  if (!my_share(a, lane, total, me, u, u_end)) return;
 
   while (u < u_end) {
     const Piece p = next_piece(a, lane, u, u_end);
+    note_tile(a, total, me, p);
     const uint16_t* kh = a.k + (int64_t)p.kvh * a.k_h;
     const uint16_t* vh = a.v + (int64_t)p.kvh * a.v_h;
     const int row0 = p.row0 + 16 * RT * wave;
@@ -662,60 +701,88 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
 }
 
 // ------------------------------------------------------------------------------ the join
-// One wave per query row and head: the parts of its tile, in key order.  HD / 64 elements a lane.
-template <int HD, bool BF16>
-__global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
-  constexpr int E = HD / 64;
-  const int R = a.R;
-  const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t total = total_units(a, lane);
-  if (total == 0 || id >= (int64_t)a.N * a.hq) return;
-  const int64_t n = shares(a, total);
-  const int tok = (int)(id / a.hq), head = (int)(id - (int64_t)tok * a.hq);
+// Grid x: tiles (the kernels note how many there are; past the grid, in turn), y: blocks of rows.  HD / 8
+// lanes to a row, 8 columns each.  SPLIT: the four waves take every fourth part of the same rows
+// and meet in LDS; otherwise each has rows of its own.  Where a workgroup's share is a small part
+// of a tile there are many parts and few tiles (64 parts for 131072 keys of one sequence: 9 us
+// split, 35 us one wave a row); where shares and tiles are alike, two parts and many rows (512 rows
+// of 64 tiles: 20 us and 31 us split).
+template <int HD, bool SPLIT>
+constexpr int join_rows() { return (SPLIT ? 64 : 256) / (HD / 8); }
 
-  // the sequence of the token: the first whose query rows end past it, and the units before it
-  int b = -1;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int64_t own = 0;
-    bool has = false;
-    if (b0 + lane < a.B) {
-      const Seq s = sequence(a, b0 + lane);
-      own = (int64_t)s.tiles * s.units * a.hkv;
-      has = tok >= s.q0 && tok < s.q0 + s.tokens;
+template <int HD, bool BF16, bool SPLIT>
+__global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
+  constexpr int TPR = HD / 8, U = SPLIT ? 8 : 4;  // U: parts in flight
+  __shared__ __align__(16) float sums[SPLIT ? 4 : 1][64][12];  // of each lane: 8 columns, the base, the sum
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row = blockIdx.y * join_rows<HD, SPLIT>() + (SPLIT ? lane : (int)threadIdx.x) / TPR, c = lane % TPR;
+  const int tiles = *a.tiles, step = SPLIT ? 4 : 1;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const Cut cut = a.cuts[tile];
+    if (cut.parts == 0) continue;
+    // part 0 is the first workgroup's second, part i the first of the workgroup i places on
+    auto place = [&](int i) { return ((int64_t)2 * (cut.first + i) + (i == 0 ? 1 : 0)) * a.R + row; };
+    const bool live = cut.row0 + row < cut.rows;
+    float base = kNone, sum = 0.f;
+    f32x4_t y0 = f32x4_t{0.f, 0.f, 0.f, 0.f}, y1 = y0;
+    for (int i0 = SPLIT ? wave : 0; live && i0 < cut.parts; i0 += U * step) {
+      float ml[U][2], top = base;
+      f32x4_t t0[U], t1[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {  // past the last part: it again, with no weight
+        const int64_t at = place(min(i0 + step * i, cut.parts - 1));
+        ml[i][0] = a.part_ml[2 * at];
+        ml[i][1] = a.part_ml[2 * at + 1];
+        t0[i] = *(const f32x4_t*)(a.part + at * HD + 8 * c);
+        t1[i] = *(const f32x4_t*)(a.part + at * HD + 8 * c + 4);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) top = fmaxf(top, ml[i][0]);
+      const float off = top == kNone ? 0.f : top, keep = __builtin_amdgcn_exp2f(base - off);
+      base = top;
+      sum *= keep;
+      y0 *= keep;
+      y1 *= keep;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (i0 + step * i < cut.parts) {
+          const float f = __builtin_amdgcn_exp2f(ml[i][0] - off);
+          sum += f * ml[i][1];
+          y0 += f * t0[i];
+          y1 += f * t1[i];
+        }
     }
-    const uint64_t at = __ballot(has);
-    if (at) {
-      b = b0 + __builtin_ctzll(at);
-      before += wave_sum(b0 + lane < b ? own : 0);
-      break;
+    if constexpr (SPLIT) {
+      float* mine = sums[wave][lane];
+      *(f32x4_t*)mine = y0;
+      *(f32x4_t*)(mine + 4) = y1;
+      mine[8] = base;
+      mine[9] = sum;
+      __syncthreads();
+      float top = kNone;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, sums[w][lane][8]);
+      const float off = top == kNone ? 0.f : top;
+      sum = 0.f;
+      y0 = y1 = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sums[w][lane][8] - off);
+        sum += f * sums[w][lane][9];
+        y0 += f * *(const f32x4_t*)sums[w][lane];
+        y1 += f * *(const f32x4_t*)(sums[w][lane] + 4);
+      }
+      __syncthreads();  // read before the next tile's
     }
-    before += wave_sum(own);
+    if (live && (!SPLIT || wave == 0)) {
+      const float inv = inverse(sum);
+      const int tok = (int)divide((uint32_t)(cut.row0 + row), a.by_group);
+      const int head = cut.kvh * a.group + cut.row0 + row - tok * a.group;
+      *(u32x4_t*)(a.out + (int64_t)(cut.q0 + tok) * a.o_t + (int64_t)head * a.o_h + 8 * c) =
+          u32x4_t{pack2<BF16>(y0[0] * inv, y0[1] * inv), pack2<BF16>(y0[2] * inv, y0[3] * inv),
+                  pack2<BF16>(y1[0] * inv, y1[1] * inv), pack2<BF16>(y1[2] * inv, y1[3] * inv)};
+    }
   }
-  if (b < 0) return;
-  const Seq s = sequence(a, b);
-  const int kvh = head / a.group, row = (tok - s.q0) * a.group + head - kvh * a.group;
-  const int64_t u0 = before + ((int64_t)kvh * s.tiles + row / R) * s.units;
-  const int64_t i0 = share_of(total, n, u0), i1 = share_of(total, n, u0 + s.units - 1);
-  if (i0 == i1) return;  // one workgroup held the tile and wrote it
-  float top = kNone, sum = 0.f, y[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = 0.f;
-  for (int64_t i = i0; i <= i1; ++i) {
-    const int64_t at = (2 * i + (i == i0 ? 1 : 0)) * R + row % R;
-    const float pm = a.part_ml[at * 2], pl = a.part_ml[at * 2 + 1];
-    const float now = fmaxf(top, pm), base = now == kNone ? 0.f : now;
-    const float f0 = __builtin_amdgcn_exp2f(top - base), f1 = __builtin_amdgcn_exp2f(pm - base);
-    sum = sum * f0 + pl * f1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = y[e] * f0 + a.part[at * HD + lane * E + e] * f1;
-    top = now;
-  }
-  const float inv = inverse(sum);
-  uint16_t* to = a.out + (int64_t)tok * a.o_t + (int64_t)head * a.o_h + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) to[e] = f32_to_act<BF16>(y[e] * inv);
 }
 
 template <int HD, bool BF16>
@@ -739,8 +806,11 @@ hipError_t launch(const TreeArgs& a, const TreePlan& pl, hipStream_t stream) {
   void* argv[1] = {&args};
   e = hipLaunchKernel(kern, dim3((unsigned)a.blocks), dim3((unsigned)threads), argv, (size_t)lds, stream);
   if (e != hipSuccess) return e;
-  const int64_t waves = (int64_t)a.N * a.hq;
-  hipLaunchKernelGGL((tree_join_kernel<HD, BF16>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a);
+  const bool split = pl.blocks >= 4 * pl.tiles;  // four workgroups or more to a tile
+  const int join = split ? join_rows<HD, true>() : join_rows<HD, false>();
+  const dim3 grid((unsigned)std::min<int64_t>(pl.tiles, 1 << 20), (unsigned)((a.R + join - 1) / join));
+  if (split) hipLaunchKernelGGL((tree_join_kernel<HD, BF16, true>), grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((tree_join_kernel<HD, BF16, false>), grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -750,7 +820,10 @@ hipError_t launch_tree(const TreeProblem& p, const TreePlan& pl, float scale, vo
   TreeArgs a{};
   a.q = (const uint16_t*)p.q; a.k = (const uint16_t*)p.k; a.v = (const uint16_t*)p.v;
   a.table = p.table; a.context = p.context; a.starts = p.starts; a.mask = p.mask; a.out = (uint16_t*)p.out;
-  a.part = (float*)workspace;
+  static_assert(sizeof(Cut) == kTreeCutBytes, "the plan's size of the notes");
+  a.tiles = (int32_t*)workspace;
+  a.cuts = (Cut*)workspace + 1;
+  a.part = (float*)((char*)workspace + pl.notes_bytes);
   a.part_ml = a.part + pl.blocks * 2 * pl.rows * p.d;
   a.R = pl.rows; a.unit = pl.unit;
   a.q_t = p.q_t; a.q_h = p.q_h; a.k_h = p.k_h; a.v_h = p.v_h;

@@ -278,7 +278,7 @@ int validate_tree(const wq_tensor* q, const wq_tensor* k_cache, const wq_tensor*
   const int64_t B = block_table->shape[0], width = block_table->shape[1];
   if (d != 64 && d != 128 && d != 256) return WQ_ERR_PARAM_INVALID;
   if (hq < 1 || hq > 65535 || hkv < 1 || hkv > hq || hq % hkv != 0) return WQ_ERR_PARAM_INVALID;
-  if (N > (1 << 24) || B > 65535) return WQ_ERR_PARAM_INVALID;
+  if (N > (1 << 24) || N * hq > (1 << 30) || B > 65535) return WQ_ERR_PARAM_INVALID;
   if (k_cache->shape[2] != d || S % page_size != 0 || !same_shape(k_cache, v_cache) || !same_shape(q, output))
     return WQ_ERR_PARAM_INVALID;
   if (width * page_size > kMaxExtent) return WQ_ERR_PARAM_INVALID;
