@@ -27,12 +27,14 @@
 // operand of O^T += V^T P^T, if V^T takes the keys in the same order: two transpose reads of 4
 // keys each.  The weights never leave the registers.
 //
-// Scores, sums and outputs are fp32 (base 2: scale * log2(e) is folded into the scores).  The
-// running base that is taken off a row's scores follows the maximum only when that has grown by
-// more than kSlack: weights then reach 2^kSlack instead of 1, which fp32 and both 16-bit types
-// hold, and the outputs are rescaled a few times in a whole row instead of in every tile.  The
+// Scores, sums and outputs are fp32 (base 2: scale * log2(e) is folded into the scores).  The base
+// that is taken off a row's scores is the maximum of the tile that last set it.  Weights may reach
+// 2^kSlack, which fp32 and both 16-bit types hold; a tile whose weights pass that is taken again,
+// with its maximum found, the base raised and the outputs rescaled.  Most tiles thus find no
+// maximum at all, which costs as many vector instructions as the weights themselves.  The
 // weights are rounded to 16 bits for the second product: an error of at most 2^-8 (bf16) or
-// 2^-11 (fp16) of each, of the size of the result's own rounding.
+// 2^-11 (fp16) of each, of the size of the result's own rounding.  Their sums are taken of the
+// rounded weights, by the matrix cores (against ones), so that the weights add up to 1 exactly.
 #include <algorithm>
 #include <cmath>
 
@@ -73,7 +75,8 @@ struct TreeArgs {
 };
 
 constexpr int kSlots = 1024;    // keys whose slots stand in LDS at a time
-constexpr float kSlack = 8.f;   // log2 of the largest weight
+constexpr int kSlack = 8;       // log2 of the largest weight
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 constexpr float kNone = -__builtin_inff();
 
 // ------------------------------------------------------------------------------ the schedule
@@ -259,26 +262,24 @@ __device__ __forceinline__ uint32_t tile_bits(const TreeArgs& a, const Seq& s, i
   return (uint32_t)(((hi << 32) | lo) >> shift);
 }
 
-// The maximum (or sum) of a value over the four lanes l % 16 + 16 * {0, 1, 2, 3}, in all of them.
-template <bool SUM>
-__device__ __forceinline__ float across(float v) {
+// The maximum of a value over the four lanes l % 16 + 16 * {0, 1, 2, 3}, in all of them.
+__device__ __forceinline__ float across_max(float v) {
   const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  const float a = __uint_as_float(h[0]), b = __uint_as_float(h[1]);
-  v = SUM ? a + b : fmaxf(a, b);
+  v = fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
   const auto q = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  const float c = __uint_as_float(q[0]), d = __uint_as_float(q[1]);
-  return SUM ? c + d : fmaxf(c, d);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
 // What a wave keeps of its RT 16-row blocks: queries (MFMA B operands), tokens, outputs
-// (transposed: element i of o[t][d] is column 16 d + 4 (l / 16) + i of row l % 16), bases and this
-// lane's part of the sums.
+// (transposed: element i of o[t][d] is column 16 d + 4 (l / 16) + i of row l % 16), bases and sums
+// (the four elements of l alike).
 template <int HD, int RT>
 struct Rows {
   u32x4_t q[RT][HD / 32];
   int token[RT];
   f32x4_t o[RT][HD / 16];
-  float m[RT], l[RT];
+  f32x4_t l[RT];
+  float m[RT];
 };
 
 template <int HD, bool BF16, int RT>
@@ -294,86 +295,111 @@ __device__ __forceinline__ void start_rows(const TreeArgs& a, const Seq& s, int 
 #pragma unroll
     for (int j = 0; j < HD / 32; ++j) w.q[t][j] = (*(const u32x4_t*)(qr + 32 * j) & a.q_and) ^ a.q_xor;
     w.m[t] = kNone;
-    w.l[t] = 0.f;
+    w.l[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) w.o[t][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 }
 
-// A tile of KT keys for the rows of one wave.  EDGE tiles: `keys` of the tile that exist, `odd` rows of V
-// that clean_values took infinities or NaN from; draft0 is the drafted token of the tile's first key.
-template <int HD, bool BF16, int RT, int KT, bool EDGE>
-__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
+// A tile of KT keys for NT of a wave's row blocks, from block t0 on.  EDGE tiles: `keys` of the tile that
+// exist, `odd` rows of V that clean_values took infinities or NaN from; draft0 is the drafted token
+// of the tile's first key.
+template <int HD, bool BF16, int RT, int NT, int KT, bool EDGE>
+__device__ __forceinline__ void compute_rows(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
                                              uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
-                                             int lane, Rows<HD, RT>& w) {
+                                             int lane, const int t0, Rows<HD, RT>& w) {
   using C = Cfg<HD, KT>;
   constexpr int KB = KT / 16;
   asm volatile("" : "+v"(lane));  // as in load_tile
   const int l16 = lane & 15, g = lane >> 4;
-  f32x4_t sc[RT][KB];
+  uint32_t seen[NT][KT / 32];  // EDGE: bit r of word b, whether this lane's row sees key 32 b + r
+  if constexpr (EDGE)
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int h = 0; h < KB; ++h) sc[t][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < HD / 32; ++j)
-#pragma unroll
-    for (int h = 0; h < KB; ++h) {
-      const int row = 16 * h + l16;
-      const u32x4_t kf = *(const u32x4_t*)(stage + row * C::RB + 16 * k_chunk<HD>(row, 4 * j + g));
-#pragma unroll
-      for (int t = 0; t < RT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, w.q[t][j], sc[t][h]);
-    }
+      for (int b = 0; b < KT / 32; ++b)
+        seen[t][b] = (uint32_t)(keys >> (32 * b)) & tile_bits(a, s, w.token[t0 + t], draft0 + 32 * b);
 
-  uint32_t seen[RT][KT / 32];  // EDGE: bit r of word b, whether this lane's row sees key 32 b + r
-  if constexpr (EDGE) {
+  f32x4_t sc[NT][KB];
+  u32x4_t pf[NT][KT / 32];
+  auto scores = [&](int ln) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int b = 0; b < KT / 32; ++b) {
-        seen[t][b] = (uint32_t)(keys >> (32 * b)) & tile_bits(a, s, w.token[t], draft0 + 32 * b);
+      for (int h = 0; h < KB; ++h) sc[t][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+    for (int j = 0; j < HD / 32; ++j)
+#pragma unroll
+      for (int h = 0; h < KB; ++h) {
+        const int row = 16 * h + (ln & 15);
+        const u32x4_t kf = *(const u32x4_t*)(stage + row * C::RB + 16 * k_chunk<HD>(row, 4 * j + (ln >> 4)));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, w.q[t0 + t][j], sc[t][h]);
+      }
+    if constexpr (EDGE)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < KB; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (!((seen[t][b] >> (16 * h + 4 * g + i)) & 1)) sc[t][2 * b + h][i] = kNone;
+            if (!((seen[t][h / 2] >> (16 * (h & 1) + 4 * g + i)) & 1)) sc[t][h][i] = kNone;
+  };
+  u16x2_t most;  // of the weights' bits, which order like the weights (a NaN is above all)
+  auto weights = [&]() {
+    most = u16x2_t{0, 0};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float base = w.m[t0 + t] == kNone ? 0.f : w.m[t0 + t];  // no key seen so far: every weight is 0
+#pragma unroll
+      for (int h = 0; h < KB; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[t][h][i] = __builtin_amdgcn_exp2f(fmaf(sc[t][h][i], a.scale, -base));
+#pragma unroll
+      for (int b = 0; b < KT / 32; ++b) {
+        pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
+                           pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
+                           pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, pf[t][b][e]));
       }
-  }
-
-  u32x4_t pf[RT][KT / 32];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    float top = sc[t][0][0];
-#pragma unroll
-    for (int h = 0; h < KB; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][h][i]);
-    top = across<false>(top) * a.scale;
-    if (__ballot(top > w.m[t] + kSlack)) {
-      const float now = fmaxf(w.m[t], top);
-      const float keep = __builtin_amdgcn_exp2f(w.m[t] - (now == kNone ? 0.f : now));
-      w.m[t] = now;
-      w.l[t] *= keep;
-#pragma unroll
-      for (int d = 0; d < HD / 16; ++d) w.o[t][d] *= keep;
     }
-    const float base = w.m[t] == kNone ? 0.f : w.m[t];  // no key seen so far: every weight is 0
-    float sum = 0.f;
+  };
+  constexpr uint16_t kMost = BF16 ? (127 + kSlack) << 7 : (15 + kSlack) << 10;
+  bool raise = EDGE;  // a row has no base yet, or a weight is too large; edge tiles are few
 #pragma unroll
-    for (int h = 0; h < KB; ++h)
+  for (int t = 0; t < NT; ++t) raise |= w.m[t0 + t] == kNone;
+  if (!EDGE && !__ballot(raise)) {
+    scores(lane);
+    weights();
+    raise = most[0] > kMost || most[1] > kMost;
+  }
+  if (EDGE || __ballot(raise)) {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    scores(ln);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(sc[t][h][i], a.scale, -base));
-        sc[t][h][i] = p;
-        sum += p;
-      }
-    w.l[t] += sum;
+    for (int t = 0; t < NT; ++t) {
+      float top = sc[t][0][0];
+#pragma unroll
+      for (int h = 0; h < KB; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][h][i]);
+      const float now = fmaxf(w.m[t0 + t], across_max(top) * a.scale);
+      const float keep = __builtin_amdgcn_exp2f(w.m[t0 + t] - (now == kNone ? 0.f : now));
+      w.m[t0 + t] = now;
+      w.l[t0 + t] *= keep;
+#pragma unroll
+      for (int d = 0; d < HD / 16; ++d) w.o[t0 + t][d] *= keep;
+    }
+    weights();
+  }
+  constexpr uint32_t kOne2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int b = 0; b < KT / 32; ++b)
-      pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
-                         pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
-                         pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
-  }
+      w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pf[t][b], w.l[t0 + t]);
 
   // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3 of each 32
   const uint8_t* vs = stage + C::Half;
@@ -388,7 +414,7 @@ __device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, co
       const u32x2_t v1 = lds_read_tr16(vs + r1 * C::RB + 16 * v_chunk<HD>(r1, c) + vhalf);
       const u32x4_t vf = u32x4_t{v0[0], v0[1], v1[0], v1[1]};
 #pragma unroll
-      for (int t = 0; t < RT; ++t) w.o[t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t][d]);
+      for (int t = 0; t < NT; ++t) w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t0 + t][d]);
     }
   }
 
@@ -398,7 +424,7 @@ __device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, co
       odd &= odd - 1;
       const uint16_t* vr = (const uint16_t*)((const uint8_t*)vh + (uint64_t)(uint32_t)slots[first + r] * a.v_row) + 4 * g;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
+      for (int t = 0; t < NT; ++t) {
         float p = 0.f;  // the row's weight of key r, from the lane that has it
         uint32_t sees = 0;
 #pragma unroll
@@ -416,10 +442,24 @@ __device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, co
           for (int i = 0; i < 4; ++i) {
             asm volatile("" ::: "memory");  // one element at a time: this path is rare, registers are not plenty
             const uint16_t x = vr[16 * d + i];
-            if (not_finite<BF16>(x) && sees) w.o[t][d][i] += p * act_to_f32<BF16>(x);
+            if (not_finite<BF16>(x) && sees) w.o[t0 + t][d][i] += p * act_to_f32<BF16>(x);
           }
       }
     }
+  }
+}
+
+// The same for all of a wave's row blocks: at once, and edge tiles one by one, which takes fewer registers.
+template <int HD, bool BF16, int RT, int KT, bool EDGE>
+__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
+                                             uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
+                                             int lane, Rows<HD, RT>& w) {
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      compute_rows<HD, BF16, RT, 1, KT, true>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
+  } else {
+    compute_rows<HD, BF16, RT, RT, KT, false>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, 0, w);
   }
 }
 
@@ -563,7 +603,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
     float* rowsum = (float*)lds;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const float l = across<true>(w.l[t]);
+      const float l = w.l[t][0];
       const int row = wave * R + 16 * t + l16;
       if (g == 0) {
         stat[row * 2] = w.m[t];
@@ -677,7 +717,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int row = row0 + 16 * t + l16;
-      const float l = across<true>(w.l[t]);
+      const float l = w.l[t][0];
       if (row >= p.rows) continue;
       if (p.whole) {
         const float inv = inverse(l);
