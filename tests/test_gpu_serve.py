@@ -452,6 +452,32 @@ def test_tree_unseen_values_have_no_part():
                     assert (out[i, :, :40] == -inf).all() and torch.isfinite(out[i, :, 40:]).all()
 
 
+@pytest.mark.parametrize("dt", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("hq,tokens", [(2, 3), (8, 4), (8, 9), (16, 12), (16, 40)])
+def test_tree_scores_that_jump(dt, hq, tokens):
+    """Each row's scores jump by hundreds at a key of its own, anywhere in a long context and in any order, so
+    that what has been summed before has to shrink to nothing: every place of a tile in turn."""
+    say("tree jumps", dt, hq, tokens)
+    c = tree_case(81, dt, [(1500, tokens)], hq, 1, 128, 16, None)
+    g = gen(82)
+    rows = tokens * hq
+    unit = torch.nn.functional.normalize(torch.randn(rows, 128, generator=g), dim=-1)
+    c["q"] = (40 * unit).view(tokens, hq, 128).to(dt).to(DEV)
+    key = torch.randperm(1500, generator=g)[:rows]
+    slot = c["table"].cpu()[0, key // 16].long() * 16 + key % 16
+    c["k"] *= 0.05
+    c["k"][slot.to(DEV), 0] = (60 * unit).to(dt).to(DEV)
+    ref, bound = tree_ref(c)
+    close(tree_run(c), ref, bound, "jumps")
+    # the same scores growing slowly, past the slack again and again
+    ramp = torch.arange(1500) / 1500.0
+    slots = (c["table"].cpu()[0, torch.arange(1500) // 16].long() * 16 + torch.arange(1500) % 16).to(DEV)
+    c["q"] = (torch.ones(tokens, hq, 128) * 0.5).to(dt).to(DEV)
+    c["k"][slots, 0] = (ramp[:, None] * 30 * torch.ones(1500, 128)).to(dt).to(DEV)
+    ref, bound = tree_ref(c)
+    close(tree_run(c), ref, bound, "ramp")
+
+
 def test_tree_strides():
     """q as a slice of a projection, K and V interleaved in one cache, output heads first."""
     say("tree strides")

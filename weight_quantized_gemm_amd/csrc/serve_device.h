@@ -40,11 +40,13 @@ __device__ __forceinline__ u32x2_t lds_read_tr16(const uint8_t* p) {
   return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((WQ_LDS i16x4_t*)(p)));
 }
 
+// The LDS address of a pointer into it, as direct-to-LDS loads take it (for offsets to be added to).
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(WQ_LDS const void*)p; }
+
 // One 16-byte-per-lane direct-to-LDS load from 64-bit addresses (a cache passes 4 GiB): lane
-// l's 16 bytes land at lds_block + 16 * l.  Self-contained like dma16 (wq_device.h); the caller
+// l's 16 bytes land at LDS address lds + 16 * l.  Self-contained like dma16 (wq_device.h); the caller
 // counts it in its vmcnt waits.
-__device__ __forceinline__ void dma16_global(const void* src, const void* lds_block) {
-  const uint32_t lds = (uint32_t)(uintptr_t)(WQ_LDS const void*)lds_block;
+__device__ __forceinline__ void dma16_global(const void* src, uint32_t lds) {
   uint32_t saved;
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
@@ -55,6 +57,12 @@ __device__ __forceinline__ void dma16_global(const void* src, const void* lds_bl
       : "=&s"(saved)
       : "s"((uint32_t)__builtin_amdgcn_readfirstlane((int)lds)), "v"((uint64_t)src)
       : "memory");
+}
+
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | ((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32));
 }
 
 }  // namespace wq

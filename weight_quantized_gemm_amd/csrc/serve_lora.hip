@@ -157,7 +157,7 @@ template <bool BF16, int W, int MT, int NT, int NW>
 __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int64_t w0, int m0, int key, uint64_t rows,
                                             int r0, int kb, int ke, float* h) {
   using S = ShrinkStage<MT, NT>;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   f32x4_t acc[MT][NT];
 #pragma unroll
@@ -175,9 +175,10 @@ __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int
     else src[i] = p.a + ((int64_t)key * p.r + min(r0 + row - 16 * MT, p.r - 1)) * p.k + c;
   }
   uint8_t* mine = lds + wave * 2 * S::Bytes;
+  const uint32_t to = lds_address(lds) + wave * 2 * S::Bytes;
   const int full = (ke - kb) / 64;  // whole steps; the waves take them in turn from step `turn` on
   const int turn = (int)(w0 / W % 1024) * NW;
-  auto load = [&](int i, uint8_t* stage) {
+  auto load = [&](int i, uint32_t stage) {
     const int k0 = kb + 64 * (int)((uint32_t)(i + turn) % (uint32_t)full);
 #pragma unroll
     for (int l = 0; l < S::Loads; ++l) dma16_global(src[l] + k0, stage + 1024 * l);
@@ -200,10 +201,10 @@ __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int
   __syncthreads();  // the LDS has been read
   wave_wait<0>();
   int st = 0;
-  if (wave < full) load(wave, mine);
+  if (wave < full) load(wave, to);
   for (int i = wave; i < full; i += NW, st ^= 1) {
     if (i + NW < full) {
-      load(i + NW, mine + (st ^ 1) * S::Bytes);
+      load(i + NW, to + (st ^ 1) * S::Bytes);
       wave_wait<S::Loads>();
     } else {
       wave_wait<0>();
@@ -258,16 +259,19 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const Lo
   constexpr int NW = kShrinkWaves;
   for_items<W>(p, p.splits * p.rank_blocks, [&](const Item& it, int part) {
     const int split = part % p.splits, r0 = part / p.splits * (16 * NT);
-    if (r0 >= it.rank) return;
+    if (r0 >= uniform(it.rank)) return;
+    const int key = uniform(it.key);
+    const uint64_t rows = (uint64_t)uniform((int64_t)it.rows);
+    const int64_t w0 = uniform(it.w0);
     const int kb = split * p.kchunk, ke = min(p.k, kb + p.kchunk);
     float* h = p.h + (int64_t)split * p.m * p.r;
     if constexpr (W == 16) {
-      shrink_item<BF16, W, 1, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
+      shrink_item<BF16, W, 1, NT, NW>(p, lds, w0, 0, key, rows, r0, kb, ke, h);
     } else {
       // rows inside one 16-row block (single tokens, the ends of prompts) read that block only
-      const int lo = __builtin_ctzll(it.rows) >> 4, hi = (63 - __builtin_clzll(it.rows)) >> 4;
-      if (lo == hi) shrink_item<BF16, W, 1, NT, NW>(p, lds, it.w0, lo, it.key, it.rows, r0, kb, ke, h);
-      else shrink_item<BF16, W, 4, NT, NW>(p, lds, it.w0, 0, it.key, it.rows, r0, kb, ke, h);
+      const int lo = __builtin_ctzll(rows) >> 4, hi = (63 - __builtin_clzll(rows)) >> 4;
+      if (lo == hi) shrink_item<BF16, W, 1, NT, NW>(p, lds, w0, lo, key, rows, r0, kb, ke, h);
+      else shrink_item<BF16, W, 4, NT, NW>(p, lds, w0, 0, key, rows, r0, kb, ke, h);
     }
   });
 }
@@ -307,20 +311,21 @@ template <bool BF16, int W, int CH>
 __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expand_kernel(const LoraArgs p) {
   extern __shared__ __align__(16) uint8_t stages[];
   constexpr int MT = W / 16, Stage = 32 * CH * 16, Loads = Stage / 1024, RB = 8 * CH;  // RB: ranks of a stage
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int r16 = (p.r + 15) & ~15, hp = r16 + 4;
   float* sums = (float*)(stages + 8 * Stage) + wave * (16 * kSumRow);
   uint32_t* lds = (uint32_t*)(stages + 8 * Stage + 4 * 16 * kSumRow * 4);
   float* factor = (float*)(lds + W * hp);
   uint8_t* mine = stages + wave * 2 * Stage;
+  const uint32_t to = lds_address(stages) + wave * 2 * Stage;
   for_items<W>(p, p.col_blocks, [&](const Item& it, int part) {
-    const int key = it.key;
-    const uint64_t rows = it.rows;
-    const int64_t w0 = it.w0;
+    const int key = uniform(it.key);
+    const uint64_t rows = (uint64_t)uniform((int64_t)it.rows);
+    const int64_t w0 = uniform(it.w0);
     const int64_t n1 = min(p.n, ((int64_t)part + 1) * p.cols);
     int64_t nc = (int64_t)part * p.cols + wave * 32;
-    const int rank = it.rank;
+    const int rank = uniform(it.rank);
     if (rank == 0 && p.x3 == p.out) return;  // nothing to add in place
     const int nk = (rank + 15) / 16, steps = (rank + RB - 1) / RB;
 
@@ -337,7 +342,7 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
           x[t] = *(const u32x4_t*)(p.x3 + min(w0 + 16 * t + row4, p.m - 1) * p.s3 + min(nc + col4, p.n - 8));
       }
     };
-    auto load_b = [&](int64_t nc, int r0, uint8_t* stage) {  // ranks r0 .. + RB - 1
+    auto load_b = [&](int64_t nc, int r0, uint32_t stage) {  // ranks r0 .. + RB - 1
 #pragma unroll
       for (int i = 0; i < Loads; ++i) {
         const int e = 64 * i + lane, n = e / CH, c = (e % CH) ^ (column_turn(n) & (CH - 1));
@@ -347,7 +352,7 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
     const bool busy = nc < n1;
     if (busy) {  // on their way while h is made ready
       load_x(nc);
-      if (rank) load_b(nc, 0, mine);
+      if (rank) load_b(nc, 0, to);
     }
 
     if (rank) {  // h of the adapter's rows: splits added in order, scaled, split into hi + lo
@@ -417,7 +422,7 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
       for (int s = 0; s < steps; ++s, st ^= 1) {
         const bool last = s + 1 == steps;
         if (!last || nc + kLoraCols < n1) {
-          load_b(last ? nc + kLoraCols : nc, last ? 0 : RB * (s + 1), mine + (st ^ 1) * Stage);
+          load_b(last ? nc + kLoraCols : nc, last ? 0 : RB * (s + 1), to + (st ^ 1) * Stage);
           wave_wait<Loads>();
         } else {
           wave_wait<0>();

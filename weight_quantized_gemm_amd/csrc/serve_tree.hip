@@ -142,8 +142,8 @@ __device__ __forceinline__ int find_sequence(const TreeArgs& a, int lane, int64_
     const uint64_t past = __ballot(base + c.units > u);
     if (past) {
       const int at = __builtin_ctzll(past);
-      before = base + __shfl(c.units - units_of(a, c.mine), at, 64);
-      tiles_before = tiles + __shfl(c.tiles - (int64_t)c.mine.tiles * a.hkv, at, 64);
+      before = uniform(base + __shfl(c.units - units_of(a, c.mine), at, 64));
+      tiles_before = uniform(tiles + __shfl(c.tiles - (int64_t)c.mine.tiles * a.hkv, at, 64));
       s.q0 = __builtin_amdgcn_readlane(c.mine.q0, at);
       s.tokens = __builtin_amdgcn_readlane(c.mine.tokens, at);
       s.ctx = __builtin_amdgcn_readlane(c.mine.ctx, at);
@@ -174,28 +174,28 @@ struct Cfg {
 // 16-byte chunk c of K row r stands in slot row_slot (16-byte reads of 16 rows at one chunk hit all
 // banks); the 32-byte pair p of V row r in pair_slot (a transpose read takes 32 bytes of 8 rows).
 // Rows of 512 bytes start in the same bank as rows of 256, so they take the latter's pattern.
-template <int HD> __device__ __forceinline__ int k_chunk(int r, int c) {
-  if constexpr (HD == 256) return c ^ (r & 15);
-  else return row_slot<HD * 2>(r, c);
+template <int HD> __device__ __forceinline__ uint32_t k_chunk(uint32_t r, uint32_t c) {
+  if constexpr (HD == 64) return c ^ ((r / 2) % 8);  // row_slot<128>
+  else return c ^ (r % 16);
 }
-template <int HD> __device__ __forceinline__ int v_chunk(int r, int c) {
-  if constexpr (HD == 256) return c ^ (2 * (r & 7));
-  else return 2 * pair_slot<HD * 2>(r, c >> 1) + (c & 1);
+template <int HD> __device__ __forceinline__ uint32_t v_chunk(uint32_t r, uint32_t c) {
+  if constexpr (HD == 64) return c ^ (2 * ((r / 2) % 4));  // pair_slot<128>
+  else return c ^ (2 * (r % 8));
 }
 
-// Load part `w` of `parts` of a tile: keys first + 0 .. KT - 1 of the slots in LDS.
+// Load part `w` of `parts` of a tile, to LDS address `stage`: keys first + 0 .. KT - 1 of the slots in LDS.
 template <int HD, int KT, int PARTS>
 __device__ __forceinline__ void load_tile(const TreeArgs& a, const uint16_t* kh, const uint16_t* vh, const int* slots,
-                                          int first, int count, uint8_t* stage, int w, int lane) {
+                                          int first, uint32_t stage, int w, int lane) {
   using C = Cfg<HD, KT>;
   static_assert(C::Loads % PARTS == 0, "whole loads for each wave");
   asm volatile("" : "+v"(lane));  // addresses are made anew for each tile: kept, they would take 100 registers
   stage += 1024 * (C::Loads / PARTS) * w;
-  const int e0 = 64 * (C::Loads / PARTS) * w + lane;
+  const uint32_t e0 = (uint32_t)(64 * (C::Loads / PARTS) * w + lane);
 #pragma unroll
   for (int i = 0; i < C::Loads / PARTS; ++i) {
-    const int row = (e0 + 64 * i) / C::CH, c = (e0 + 64 * i) % C::CH;
-    const uint32_t slot = (uint32_t)max(slots[min(first + row, count - 1)], 0);  // no such key: any row of the cache
+    const uint32_t row = (e0 + 64 * i) / C::CH, c = (e0 + 64 * i) % C::CH;
+    const uint32_t slot = (uint32_t)max(slots[first + row], 0);  // no such key: any row of the cache
     dma16_global((const uint8_t*)kh + (uint64_t)slot * a.k_row + 16 * k_chunk<HD>(row, c), stage + 1024 * i);
     dma16_global((const uint8_t*)vh + (uint64_t)slot * a.v_row + 16 * v_chunk<HD>(row, c), stage + C::Half + 1024 * i);
   }
@@ -212,10 +212,10 @@ __device__ __forceinline__ bool not_finite(uint32_t half) {
 // without a key and its infinities and NaN (0 * inf would reach rows that do not see them); what
 // those contribute to rows that do see them is added afterwards.
 
-// Bit r: whether key r of the tile exists (keys at or past `count` do not belong to this piece of work).
+// Bit r: whether key r of the tile exists.
 template <int KT>
-__device__ __forceinline__ uint64_t tile_keys(const int* slots, int first, int count, int lane) {
-  return __ballot(lane < KT && first + lane < count && slots[min(first + lane, kSlots - 1)] >= 0);
+__device__ __forceinline__ uint64_t tile_keys(const int* slots, int first, int lane) {
+  return __ballot(lane < KT && slots[min(first + lane, kSlots - 1)] >= 0);
 }
 
 // Part `w` of `parts` of V without what the product must not meet; returns the rows (bits) of this
@@ -301,85 +301,57 @@ __device__ __forceinline__ void start_rows(const TreeArgs& a, const Seq& s, int 
   }
 }
 
-// A tile of KT keys for NT of a wave's row blocks, from block t0 on.  EDGE tiles: `keys` of the tile that
-// exist, `odd` rows of V that clean_values took infinities or NaN from; draft0 is the drafted token
-// of the tile's first key.
-template <int HD, bool BF16, int RT, int NT, int KT, bool EDGE>
-__device__ __forceinline__ void compute_rows(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
+// A tile of KT keys for NT of a wave's row blocks, from block t0 on.
+//
+// SLOW: finds the rows' maxima, raises their bases and rescales what has been summed; and of an edge
+// tile it takes `keys` that exist, drafted tokens from draft0 on (the tile's first key; at most -KT: none),
+// and the rows `odd` of V that clean_values took infinities or NaN from.  Otherwise all keys are seen and
+// the bases stay; returns false, with nothing summed, where a row has no base yet or a weight
+// passes 2^kSlack.
+template <int HD, bool BF16, int RT, int NT, int KT, bool SLOW>
+__device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
                                              uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
                                              int lane, const int t0, Rows<HD, RT>& w) {
   using C = Cfg<HD, KT>;
   constexpr int KB = KT / 16;
+  if constexpr (!SLOW) {
+    bool unset = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) unset |= w.m[t0 + t] == kNone;
+    if (__ballot(unset)) return false;
+  }
   asm volatile("" : "+v"(lane));  // as in load_tile
   const int l16 = lane & 15, g = lane >> 4;
-  uint32_t seen[NT][KT / 32];  // EDGE: bit r of word b, whether this lane's row sees key 32 b + r
-  if constexpr (EDGE)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int b = 0; b < KT / 32; ++b)
-        seen[t][b] = (uint32_t)(keys >> (32 * b)) & tile_bits(a, s, w.token[t0 + t], draft0 + 32 * b);
-
   f32x4_t sc[NT][KB];
-  u32x4_t pf[NT][KT / 32];
-  auto scores = [&](int ln) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int h = 0; h < KB; ++h) sc[t][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < KB; ++h) sc[t][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // row 16 h + l16's chunk 4 j + g: the places of rows 16 apart are alike, and those of chunks 4 apart
+  // differ by an exclusive or
+  const uint32_t k0 = l16 * C::RB + 16 * k_chunk<HD>(l16, g);
 #pragma unroll
-    for (int j = 0; j < HD / 32; ++j)
+  for (int j = 0; j < HD / 32; ++j)
 #pragma unroll
-      for (int h = 0; h < KB; ++h) {
-        const int row = 16 * h + (ln & 15);
-        const u32x4_t kf = *(const u32x4_t*)(stage + row * C::RB + 16 * k_chunk<HD>(row, 4 * j + (ln >> 4)));
+    for (int h = 0; h < KB; ++h) {
+      const u32x4_t kf = *(const u32x4_t*)(stage + (k0 ^ (64 * j)) + 16 * h * C::RB);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, w.q[t0 + t][j], sc[t][h]);
-      }
-    if constexpr (EDGE)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int h = 0; h < KB; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!((seen[t][h / 2] >> (16 * (h & 1) + 4 * g + i)) & 1)) sc[t][h][i] = kNone;
-  };
-  u16x2_t most;  // of the weights' bits, which order like the weights (a NaN is above all)
-  auto weights = [&]() {
-    most = u16x2_t{0, 0};
+      for (int t = 0; t < NT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, w.q[t0 + t][j], sc[t][h]);
+    }
+
+  uint32_t seen[NT][KT / 32];  // SLOW: bit r of word b, whether this lane's row sees key 32 b + r
+  if constexpr (SLOW) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float base = w.m[t0 + t] == kNone ? 0.f : w.m[t0 + t];  // no key seen so far: every weight is 0
-#pragma unroll
-      for (int h = 0; h < KB; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[t][h][i] = __builtin_amdgcn_exp2f(fmaf(sc[t][h][i], a.scale, -base));
 #pragma unroll
       for (int b = 0; b < KT / 32; ++b) {
-        pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
-                           pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
-                           pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
+        seen[t][b] = (uint32_t)(keys >> (32 * b)) & tile_bits(a, s, w.token[t0 + t], draft0 + 32 * b);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, pf[t][b][e]));
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!((seen[t][b] >> (16 * h + 4 * g + i)) & 1)) sc[t][2 * b + h][i] = kNone;
       }
-    }
-  };
-  constexpr uint16_t kMost = BF16 ? (127 + kSlack) << 7 : (15 + kSlack) << 10;
-  bool raise = EDGE;  // a row has no base yet, or a weight is too large; edge tiles are few
-#pragma unroll
-  for (int t = 0; t < NT; ++t) raise |= w.m[t0 + t] == kNone;
-  if (!EDGE && !__ballot(raise)) {
-    scores(lane);
-    weights();
-    raise = most[0] > kMost || most[1] > kMost;
-  }
-  if (EDGE || __ballot(raise)) {
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    scores(ln);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
       float top = sc[t][0][0];
 #pragma unroll
       for (int h = 0; h < KB; ++h)
@@ -392,8 +364,35 @@ __device__ __forceinline__ void compute_rows(const TreeArgs& a, const Seq& s, co
 #pragma unroll
       for (int d = 0; d < HD / 16; ++d) w.o[t0 + t][d] *= keep;
     }
-    weights();
   }
+
+  u32x4_t pf[NT][KT / 32];
+  u16x2_t most = {0, 0};  // of the weights' bits, which order like the weights (a NaN is above all)
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float base = SLOW && w.m[t0 + t] == kNone ? 0.f : w.m[t0 + t];  // no key seen so far: every weight is 0
+#pragma unroll
+    for (int h = 0; h < KB; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[t][h][i] = __builtin_amdgcn_exp2f(fmaf(sc[t][h][i], a.scale, -base));
+#pragma unroll
+    for (int b = 0; b < KT / 32; ++b) {
+      pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
+                         pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
+                         pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
+      asm volatile("" : "+v"(pf[t][b]));  // rounded once: it is not made again for the product
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = pf[t][b][e];
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, two));
+      }
+    }
+  }
+  if constexpr (!SLOW) {
+    constexpr uint16_t kMost = BF16 ? (127 + kSlack) << 7 : (15 + kSlack) << 10;
+    if (__ballot(most[0] > kMost || most[1] > kMost)) return false;
+  }
+
   constexpr uint32_t kOne2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -401,24 +400,22 @@ __device__ __forceinline__ void compute_rows(const TreeArgs& a, const Seq& s, co
     for (int b = 0; b < KT / 32; ++b)
       w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pf[t][b], w.l[t0 + t]);
 
-  // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3 of each 32
+  // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3 of each 32; rows 16 apart and columns 16
+  // apart as above
+  const uint32_t vr = 4 * g + (l16 >> 2), v0 = vr * C::RB + 16 * v_chunk<HD>(vr, (l16 & 3) >> 1) + 8 * (l16 & 1);
   const uint8_t* vs = stage + C::Half;
-  const int vhalf = 8 * (l16 & 1);
 #pragma unroll
-  for (int b = 0; b < KT / 32; ++b) {
-    const int r0 = 32 * b + 4 * g + (l16 >> 2), r1 = r0 + 16;
+  for (int b = 0; b < KT / 32; ++b)
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) {
-      const int c = 2 * d + ((l16 & 3) >> 1);
-      const u32x2_t v0 = lds_read_tr16(vs + r0 * C::RB + 16 * v_chunk<HD>(r0, c) + vhalf);
-      const u32x2_t v1 = lds_read_tr16(vs + r1 * C::RB + 16 * v_chunk<HD>(r1, c) + vhalf);
-      const u32x4_t vf = u32x4_t{v0[0], v0[1], v1[0], v1[1]};
+      const u32x2_t lo = lds_read_tr16(vs + (v0 ^ (32 * d)) + 32 * b * C::RB);
+      const u32x2_t hi = lds_read_tr16(vs + (v0 ^ (32 * d)) + (32 * b + 16) * C::RB);
+      const u32x4_t vf = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
       for (int t = 0; t < NT; ++t) w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t0 + t][d]);
     }
-  }
 
-  if constexpr (EDGE) {
+  if constexpr (SLOW) {
     while (odd) {
       const int r = __builtin_ctzll(odd);
       odd &= odd - 1;
@@ -447,20 +444,24 @@ __device__ __forceinline__ void compute_rows(const TreeArgs& a, const Seq& s, co
       }
     }
   }
+  return true;
 }
 
-// The same for all of a wave's row blocks: at once, and edge tiles one by one, which takes fewer registers.
-template <int HD, bool BF16, int RT, int KT, bool EDGE>
-__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
-                                             uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
-                                             int lane, Rows<HD, RT>& w) {
-  if constexpr (EDGE) {
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      compute_rows<HD, BF16, RT, 1, KT, true>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
-  } else {
-    compute_rows<HD, BF16, RT, RT, KT, false>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, 0, w);
+// All of a wave's row blocks: at once where that will do, and otherwise one by one, which takes fewer
+// registers.
+template <int HD, bool BF16, int RT, int KT>
+__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, bool edge,
+                                             int draft0, uint64_t keys, uint64_t odd, const uint8_t* stage,
+                                             const uint16_t* vh, int lane, Rows<HD, RT>& w) {
+  if (!edge) {
+    if (compute_rows<HD, BF16, RT, RT, KT, false>(a, s, slots, first, 0, 0, 0, stage, vh, lane, 0, w)) return;
+    keys = ~0ull;
+    odd = 0;
+    draft0 = -KT;
   }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+    compute_rows<HD, BF16, RT, 1, KT, true>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
 }
 
 // 1 / sum; no key seen: 0; NaN stays
@@ -472,7 +473,7 @@ struct Piece {
   Seq s;
   int b, kvh, row0, rows;      // rows: of the sequence and cached head
   int key_lo, key_hi;
-  bool whole, begins;          // all units of the tile; its first unit
+  int whole, begins;           // whether all units of the tile, and its first
   int64_t tile_end, tile_id;   // the unit past the tile; its place among all tiles
 };
 
@@ -484,32 +485,37 @@ __device__ __forceinline__ Piece next_piece(const TreeArgs& a, int lane, int64_t
   const int64_t in = u - before;
   const int tile = (int)(in / p.s.units), u0 = (int)(in - (int64_t)tile * p.s.units);
   const int u1 = (int)min((int64_t)p.s.units, u0 + (u_end - u));
-  u += u1 - u0;
-  p.kvh = tile / p.s.tiles;
-  p.row0 = (tile - p.kvh * p.s.tiles) * a.R;
+  u = uniform(u + u1 - u0);
+  p.kvh = uniform(tile / p.s.tiles);
+  p.row0 = uniform((tile - p.kvh * p.s.tiles) * a.R);
   p.rows = p.s.tokens * a.group;
-  p.key_lo = u0 * a.unit;
-  p.key_hi = (int)min((int64_t)p.s.len, (int64_t)u1 * a.unit);
+  p.key_lo = uniform(u0 * a.unit);
+  int key_hi = (int)min((int64_t)p.s.len, (int64_t)u1 * a.unit);
   if (!a.has_mask) {  // a chain's rows see no key past their last token
     const int last = (int)divide((uint32_t)min(p.row0 + a.R, p.rows) - 1, a.by_group);
-    p.key_hi = (int)min((int64_t)p.key_hi, (int64_t)p.s.ctx + last + 1);
+    key_hi = (int)min((int64_t)key_hi, (int64_t)p.s.ctx + last + 1);
   }
-  p.tile_end = before + (int64_t)(tile + 1) * p.s.units;
-  p.tile_id = tiles_before + tile;
-  p.whole = u0 == 0 && u1 == p.s.units;
-  p.begins = u0 == 0;
+  p.key_hi = uniform(key_hi);
+  p.tile_end = uniform(before + (int64_t)(tile + 1) * p.s.units);
+  p.tile_id = uniform(tiles_before + tile);
+  p.whole = uniform(u0 == 0 && u1 == p.s.units);
+  p.begins = uniform(u0 == 0);
   return p;
 }
 
-// The slots of keys key0 .. + count - 1 of sequence b, -1 on no page; returns whether any is.
+// The slots of keys key0 .. + count - 1 of sequence b, -1 for one on no page and for those that fill the
+// last tile; returns whether a key is on no page.
 __device__ __forceinline__ int find_slots(const TreeArgs& a, int b, int key0, int count, int* slots, int tid, int threads) {
   int lost = 0;
-  for (int i = tid; i < count; i += threads) {
-    const uint32_t key = (uint32_t)(key0 + i), page = divide(key, a.by_page);
-    const int e = a.table[(int64_t)b * a.width + page];
-    const bool ok = e >= 0 && e < a.pages;
-    slots[i] = ok ? (int)((uint32_t)e * a.by_page.d + (key - page * a.by_page.d)) : -1;
-    lost |= !ok;
+  for (int i = tid; i < (count + 63) / 64 * 64; i += threads) {
+    int slot = -1;
+    if (i < count) {
+      const uint32_t key = (uint32_t)(key0 + i), page = divide(key, a.by_page);
+      const int e = a.table[(int64_t)b * a.width + page];
+      if (e >= 0 && e < a.pages) slot = (int)((uint32_t)e * a.by_page.d + (key - page * a.by_page.d));
+      else lost = 1;
+    }
+    slots[i] = slot;
   }
   return lost;
 }
@@ -517,7 +523,7 @@ __device__ __forceinline__ int find_slots(const TreeArgs& a, int b, int key0, in
 // This workgroup's share of all `total` units; false: none.  Shares in a row stand on one XCD
 // (workgroups go round the 8 XCDs), so that tiles of the same keys meet in its L2.
 __device__ __forceinline__ bool my_share(const TreeArgs& a, int lane, int64_t& total, int64_t& me, int64_t& u, int64_t& u_end) {
-  total = total_units(a, lane);
+  total = uniform(total_units(a, lane));
   const int64_t n = shares(a, total);
   me = blockIdx.x;
   if (n == 0 && me == 0 && threadIdx.x == 0) *a.tiles = 0;
@@ -553,7 +559,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
   extern __shared__ __align__(16) uint8_t lds[];
   int* slots = (int*)(lds + L::Area);
   float* stat = (float*)(lds + L::Area + kSlots * 4);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int64_t total, me, u, u_end;
   if (!my_share(a, lane, total, me, u, u_end)) return;
@@ -567,32 +573,33 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
     start_rows<HD, BF16, RT>(a, p.s, p.kvh, p.row0, p.rows, lane, w);
 
     uint8_t* mine = lds + wave * 2 * C::Stage;
+    const uint32_t to = lds_address(lds) + wave * 2 * C::Stage;
     for (int key0 = p.key_lo; key0 < p.key_hi; key0 += kSlots) {
       const int count = min(kSlots, p.key_hi - key0);
       __syncthreads();  // the slots (and the joining rows in the stages) have been read
-      const int lost = __syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW));
+      const int lost = uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
       const int tiles = (count + 31) / 32;
       wave_wait<0>();  // from here on the loads in flight are the tiles'
-      if (wave < tiles) load_tile<HD, 32, 1>(a, kh, vh, slots, 32 * wave, count, mine, 0, lane);
+      if (wave < tiles) load_tile<HD, 32, 1>(a, kh, vh, slots, 32 * wave, to, 0, lane);
       int st = 0;
       for (int j = wave; j < tiles; j += NW, st ^= 1) {
         const int first = 32 * j;
         if (j + NW < tiles) {
-          load_tile<HD, 32, 1>(a, kh, vh, slots, first + 32 * NW, count, mine + (st ^ 1) * C::Stage, 0, lane);
+          load_tile<HD, 32, 1>(a, kh, vh, slots, first + 32 * NW, to + (st ^ 1) * C::Stage, 0, lane);
           wave_wait<2 * C::Loads>();
         } else {
           wave_wait<0>();
         }
         uint8_t* stage = mine + st * C::Stage;
         const int draft0 = key0 + first - p.s.ctx;
-        if (lost || first + 32 > count || draft0 + 32 > 0) {
-          const uint64_t keys = tile_keys<32>(slots, first, count, lane);
-          const uint64_t odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
+        const bool edge = lost || first + 32 > count || draft0 + 32 > 0;
+        uint64_t keys = 0, odd = 0;
+        if (edge) {
+          keys = tile_keys<32>(slots, first, lane);
+          odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
           __builtin_amdgcn_wave_barrier();
-          compute_tile<HD, BF16, RT, 32, true>(a, p.s, slots, first, draft0, keys, odd, stage, vh, lane, w);
-        } else {
-          compute_tile<HD, BF16, RT, 32, false>(a, p.s, slots, first, draft0, 0, 0, stage, vh, lane, w);
         }
+        compute_tile<HD, BF16, RT, 32>(a, p.s, slots, first, edge, draft0, keys, odd, stage, vh, lane, w);
         // every read of this stage has returned before the next load into it
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
@@ -670,7 +677,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
   extern __shared__ __align__(16) uint8_t lds[];
   int* slots = (int*)(lds + RowsLds<HD, NW>::Area);
   uint64_t* odd_of = (uint64_t*)(slots + kSlots);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int64_t total, me, u, u_end;
   if (!my_share(a, lane, total, me, u, u_end)) return;
@@ -686,30 +693,30 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
     for (int key0 = p.key_lo; key0 < p.key_hi; key0 += kSlots) {
       const int count = min(kSlots, p.key_hi - key0);
       __syncthreads();  // the slots and stages have been read
-      const int lost = __syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW));
+      const int lost = uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
       const int tiles = (count + KT - 1) / KT;
       wave_wait<0>();
-      load_tile<HD, KT, NW>(a, kh, vh, slots, 0, count, lds, wave, lane);
+      const uint32_t to = lds_address(lds);
+      load_tile<HD, KT, NW>(a, kh, vh, slots, 0, to, wave, lane);
       for (int j = 0; j < tiles; ++j) {
         const int first = KT * j;
         uint8_t* stage = lds + (j & 1) * C::Stage;
         // this tile has landed for every wave, and every wave has read the one before it
         stage_barrier<0>();
         if (j + 1 < tiles)
-          load_tile<HD, KT, NW>(a, kh, vh, slots, first + KT, count, lds + ((j + 1) & 1) * C::Stage, wave, lane);
+          load_tile<HD, KT, NW>(a, kh, vh, slots, first + KT, to + ((j + 1) & 1) * C::Stage, wave, lane);
         const int draft0 = key0 + first - p.s.ctx;
-        if (lost || first + KT > count || draft0 + KT > 0) {
-          const uint64_t keys = tile_keys<KT>(slots, first, count, lane);
+        const bool edge = lost || first + KT > count || draft0 + KT > 0;
+        uint64_t keys = 0, odd = 0;
+        if (edge) {
+          keys = tile_keys<KT>(slots, first, lane);
           const uint64_t mine = clean_values<HD, BF16, KT, NW>(stage, keys, wave, lane);
           if (lane == 0) odd_of[wave] = mine;
           __syncthreads();
-          uint64_t odd = 0;
 #pragma unroll
           for (int i = 0; i < NW; ++i) odd |= odd_of[i];
-          compute_tile<HD, BF16, RT, KT, true>(a, p.s, slots, first, draft0, keys, odd, stage, vh, lane, w);
-        } else {
-          compute_tile<HD, BF16, RT, KT, false>(a, p.s, slots, first, draft0, 0, 0, stage, vh, lane, w);
         }
+        compute_tile<HD, BF16, RT, KT>(a, p.s, slots, first, edge, draft0, keys, odd, stage, vh, lane, w);
       }
     }
 
