@@ -447,14 +447,19 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
   return true;
 }
 
-// All of a wave's row blocks: at once where that will do, and otherwise one by one, which takes fewer
-// registers.
+// All of a wave's row blocks: at once, where that will do (false: nothing was done) ...
 template <int HD, bool BF16, int RT, int KT>
-__device__ __forceinline__ void compute_tile(const TreeArgs& a, const Seq& s, const int* slots, int first, bool edge,
+__device__ __forceinline__ bool compute_fast(const TreeArgs& a, const uint8_t* stage, int lane, Rows<HD, RT>& w) {
+  return compute_rows<HD, BF16, RT, RT, KT, false>(a, Seq{}, nullptr, 0, 0, 0, 0, stage, nullptr, lane, 0, w);
+}
+// ... or one by one, which takes fewer registers.  The loops over tiles below keep to the first form
+// and leave for the second: in one loop with both, the outputs would change registers at every
+// tile (40 moves).
+template <int HD, bool BF16, int RT, int KT>
+__device__ __forceinline__ void compute_slow(const TreeArgs& a, const Seq& s, const int* slots, int first, bool edge,
                                              int draft0, uint64_t keys, uint64_t odd, const uint8_t* stage,
                                              const uint16_t* vh, int lane, Rows<HD, RT>& w) {
   if (!edge) {
-    if (compute_rows<HD, BF16, RT, RT, KT, false>(a, s, slots, first, 0, 0, 0, stage, vh, lane, 0, w)) return;
     keys = ~0ull;
     odd = 0;
     draft0 = -KT;
@@ -581,8 +586,9 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
       const int tiles = (count + 31) / 32;
       wave_wait<0>();  // from here on the loads in flight are the tiles'
       if (wave < tiles) load_tile<HD, 32, 1>(a, kh, vh, slots, 32 * wave, to, 0, lane);
-      int st = 0;
-      for (int j = wave; j < tiles; j += NW, st ^= 1) {
+      // Tiles j = wave, wave + NW, ...; stage of tile j: its turn's parity.
+      int j = wave, st = 0;
+      auto begin = [&]() {  // the next tile is on its way, this one is here; whether it is an edge tile
         const int first = 32 * j;
         if (j + NW < tiles) {
           load_tile<HD, 32, 1>(a, kh, vh, slots, first + 32 * NW, to + (st ^ 1) * C::Stage, 0, lane);
@@ -590,18 +596,30 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
         } else {
           wave_wait<0>();
         }
+        return lost || first + 32 > count || key0 + first - p.s.ctx + 32 > 0;
+      };
+      auto end = [&]() {
+        // every read of this stage has returned before the next load into it
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        j += NW;
+        st ^= 1;
+      };
+      while (j < tiles) {
+        bool edge = false;
+        for (; j < tiles; end()) {
+          edge = begin();
+          if (edge || !compute_fast<HD, BF16, RT, 32>(a, mine + st * C::Stage, lane, w)) break;
+        }
+        if (j >= tiles) break;
         uint8_t* stage = mine + st * C::Stage;
-        const int draft0 = key0 + first - p.s.ctx;
-        const bool edge = lost || first + 32 > count || draft0 + 32 > 0;
         uint64_t keys = 0, odd = 0;
         if (edge) {
-          keys = tile_keys<32>(slots, first, lane);
+          keys = tile_keys<32>(slots, 32 * j, lane);
           odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
           __builtin_amdgcn_wave_barrier();
         }
-        compute_tile<HD, BF16, RT, 32>(a, p.s, slots, first, edge, draft0, keys, odd, stage, vh, lane, w);
-        // every read of this stage has returned before the next load into it
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        compute_slow<HD, BF16, RT, 32>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+        end();
       }
     }
 
@@ -698,25 +716,33 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
       wave_wait<0>();
       const uint32_t to = lds_address(lds);
       load_tile<HD, KT, NW>(a, kh, vh, slots, 0, to, wave, lane);
-      for (int j = 0; j < tiles; ++j) {
-        const int first = KT * j;
+      int j = 0;
+      // The workgroup's waves may leave the inner loop at different tiles: a wave in compute_slow takes
+      // part in the barriers of its next tile when it gets there.  Only edge tiles, which are edges for
+      // all, hold barriers of their own.
+      while (j < tiles) {
+        bool edge = false;
+        for (; j < tiles; ++j) {
+          // this tile has landed for every wave, and every wave has read the one before it
+          stage_barrier<0>();
+          if (j + 1 < tiles)
+            load_tile<HD, KT, NW>(a, kh, vh, slots, KT * (j + 1), to + ((j + 1) & 1) * C::Stage, wave, lane);
+          edge = lost || KT * (j + 1) > count || key0 + KT * (j + 1) - p.s.ctx > 0;
+          if (edge || !compute_fast<HD, BF16, RT, KT>(a, lds + (j & 1) * C::Stage, lane, w)) break;
+        }
+        if (j >= tiles) break;
         uint8_t* stage = lds + (j & 1) * C::Stage;
-        // this tile has landed for every wave, and every wave has read the one before it
-        stage_barrier<0>();
-        if (j + 1 < tiles)
-          load_tile<HD, KT, NW>(a, kh, vh, slots, first + KT, to + ((j + 1) & 1) * C::Stage, wave, lane);
-        const int draft0 = key0 + first - p.s.ctx;
-        const bool edge = lost || first + KT > count || draft0 + KT > 0;
         uint64_t keys = 0, odd = 0;
         if (edge) {
-          keys = tile_keys<KT>(slots, first, lane);
+          keys = tile_keys<KT>(slots, KT * j, lane);
           const uint64_t mine = clean_values<HD, BF16, KT, NW>(stage, keys, wave, lane);
           if (lane == 0) odd_of[wave] = mine;
           __syncthreads();
 #pragma unroll
           for (int i = 0; i < NW; ++i) odd |= odd_of[i];
         }
-        compute_tile<HD, BF16, RT, KT>(a, p.s, slots, first, edge, draft0, keys, odd, stage, vh, lane, w);
+        compute_slow<HD, BF16, RT, KT>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+        ++j;
       }
     }
 
