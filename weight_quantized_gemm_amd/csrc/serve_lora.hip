@@ -9,8 +9,11 @@
 // pair.  The item's product is taken for whole 16-row blocks of the window and only the rows
 // of its adapter are stored, so a row never depends on its neighbours.  Up to kLoraSmallM
 // tokens, windows are 16 rows and every workgroup finds its window's distinct adapters by
-// itself, with one load of 16 indices and ballots: a launch less.  Beyond, windows are 64 rows,
-// a first kernel lists the items, and the workgroups of the others walk that list.
+// itself, with one load of 16 indices and ballots: a launch less.  Beyond, windows are 64 rows
+// and a first kernel lists the items; all steps of all items (64 k of the first product, 128 columns
+// of the second) then stand in one row, of which each workgroup takes an equal share.  An item
+// whose k are cut leaves a part of h from each of its workgroups, which the second product adds in
+// order.
 //
 // Both products move far more memory than they multiply; what bounds them is how the reads
 // meet the caches and channels:
@@ -50,11 +53,12 @@ struct LoraArgs {
   const int32_t* ranks;
   const uint16_t* x3;
   uint16_t* out;
-  float* h;               // [splits][m][r]
+  float* h;               // [splits or parts][m][r]
   Item* items;            // 64-row windows: the lists, and the lengths
   int32_t* count;
   int64_t m, n, sx, s3, so, windows;
   int32_t k, r, L, splits, kchunk, slots, cols, col_blocks, rank_blocks;
+  int32_t steps, shrink_blocks;  // 64-row windows: 64-k steps of an item, workgroups of the first product
 };
 
 // The adapter of this lane's row of the window at w0 (rows past m and lanes past the window:
@@ -99,47 +103,61 @@ __global__ __launch_bounds__(256) void lora_items_kernel(const LoraArgs p) {
   if (threadIdx.x == 0) p.count[blockIdx.x] = more;
 }
 
-// Calls body(item, part) for this workgroup's items, `parts` workgroups to an item, parts fastest; each
-// XCD has an eighth of the row of units.  16-row windows: one unit to a workgroup, windows x slots x
-// parts of them, and a workgroup takes every slots-th distinct adapter of its window.  64-row
-// windows: the workgroups walk the list.
-template <int W, typename Body>
-__device__ __forceinline__ void for_items(const LoraArgs& p, int parts, const Body& body) {
+// 16-row windows: calls body(item, part) for this workgroup's items, `parts` workgroups to an item, parts
+// fastest; each XCD has an eighth of the units.  One unit to a workgroup, windows x slots x parts of
+// them, and a workgroup takes every slots-th distinct adapter of its window.
+template <typename Body>
+__device__ __forceinline__ void for_window(const LoraArgs& p, int parts, const Body& body) {
   const int lane = threadIdx.x & 63;
-  if constexpr (W == 16) {
-    const uint32_t u = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
-    const int part = u % parts, slot = u / parts % p.slots;
-    const int64_t w0 = (int64_t)(u / parts / p.slots) * W;
-    const int mine = lane_key<W>(p, w0, lane);  // windows past the last have no rows
-    uint64_t left = __ballot(mine >= -1);
-    for (int s = 0; left; ++s) {
-      const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-      const uint64_t rows = __ballot(mine == key);
-      left &= ~rows;
-      if (s % p.slots == slot) body(make_item(p, w0, key, rows), part);
-    }
-  } else {
+  const uint32_t u = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int part = u % parts, slot = u / parts % p.slots;
+  const int64_t w0 = (int64_t)(u / parts / p.slots) * 16;
+  const int mine = lane_key<16>(p, w0, lane);  // windows past the last have no rows
+  uint64_t left = __ballot(mine >= -1);
+  for (int s = 0; left; ++s) {
+    const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    const uint64_t rows = __ballot(mine == key);
+    left &= ~rows;
+    if (s % p.slots == slot) body(make_item(p, w0, key, rows), part);
+  }
+}
+
+// 64-row windows: where item i stands.
+struct Lists {
+  int own, upto;  // this lane's list: its items, and those up to and with it
+  int64_t items, share;
+
+  __device__ __forceinline__ explicit Lists(const LoraArgs& p) {
     static_assert(kLoraLists == 64, "a lane for each list");
-    const int own = p.count[lane];
-    int upto = own;
+    const int lane = threadIdx.x & 63;
+    own = upto = p.count[lane];
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int t = __shfl_up(upto, o, 64);
       if (lane >= o) upto += t;
     }
-    const int64_t total = (p.windows + __shfl(upto, 63, 64)) * parts, eighth = (total + 7) / 8;
-    const int64_t share = (p.windows + kLoraLists - 1) / kLoraLists;
-    const int64_t end = min(total, ((blockIdx.x & 7) + 1) * eighth);
-    for (int64_t u = (blockIdx.x & 7) * eighth + (blockIdx.x >> 3); u < end; u += gridDim.x >> 3) {
-      int64_t i = u / parts;
-      if (i >= p.windows) {  // an item of one of the lists
-        const int e = (int)(i - p.windows), at = __builtin_ctzll(__ballot(upto > e));
-        i = p.windows + at * share * 64 + e - __shfl(upto - own, at, 64);
-      }
-      body(p.items[i], (int)(u % parts));
-    }
+    items = p.windows + uniform(__shfl(upto, 63, 64));
+    share = (p.windows + kLoraLists - 1) / kLoraLists;
   }
-}
+  __device__ __forceinline__ int64_t at(const LoraArgs& p, int64_t i) const {
+    if (i < p.windows) return i;
+    const int e = (int)(i - p.windows), l = __builtin_ctzll(__ballot(upto > e));
+    return p.windows + l * share * 64 + e - uniform(__shfl(upto - own, l, 64));
+  }
+};
+
+// Shares of the first product's steps: so many that an item is cut into at most kLoraSplits parts.
+struct Shares {
+  int64_t total, n;
+  __device__ __forceinline__ Shares(const LoraArgs& p, int64_t items) {
+    total = items * p.rank_blocks * p.steps;
+    const int64_t least = (p.steps + kLoraSplits - 3) / (kLoraSplits - 2);  // steps of a share
+    n = max((int64_t)1, min((int64_t)p.shrink_blocks, total / least));
+  }
+  __device__ __forceinline__ int64_t begin(int64_t i) const { return total * i / n; }
+  // the share that holds step s: the largest i with begin(i) <= s
+  __device__ __forceinline__ int64_t of(int64_t s) const { return ((s + 1) * n - 1) / total; }
+};
 
 // ------------------------------------------------------------------------------- h = x1 A^T
 // A wave's stage is a step of 64 k: 16 MT rows of x1, then 16 NT rows of A_i, 128 bytes each, with
@@ -149,7 +167,7 @@ struct ShrinkStage {
   static constexpr int X = MT * 2048, Bytes = (MT + NT) * 2048, Loads = 2 * (MT + NT);
 };
 
-// One item's h for NT 16-rank tiles from rank r0 and the workgroup's k chunk.  MT 16-row blocks
+// One item's h for NT 16-rank tiles from rank r0 and k kb .. ke - 1.  MT 16-row blocks
 // from row w0 + 16 * m0.  The NW waves take 64-k steps in turn, two 16x16x32 MFMAs each (rows of
 // x1 against rows of A_i), the next step on its way meanwhile, and their sums meet in LDS, in
 // wave order.
@@ -177,7 +195,7 @@ __device__ __forceinline__ void shrink_item(const LoraArgs& p, uint8_t* lds, int
   uint8_t* mine = lds + wave * 2 * S::Bytes;
   const uint32_t to = lds_address(lds) + wave * 2 * S::Bytes;
   const int full = (ke - kb) / 64;  // whole steps; the waves take them in turn from step `turn` on
-  const int turn = (int)(w0 / W % 1024) * NW;
+  const int turn = W == 16 ? (int)(w0 / W % 1024) * NW : 0;  // (equal shares begin at different k by themselves)
   auto load = [&](int i, uint32_t stage) {
     const int k0 = kb + 64 * (int)((uint32_t)(i + turn) % (uint32_t)full);
 #pragma unroll
@@ -252,28 +270,44 @@ constexpr int shrink_lds() {
   return kShrinkWaves * std::max(2 * ShrinkStage<W / 16, NT>::Bytes, 1024 * (W / 16) * NT);
 }
 
-// Parts of an item: blocks of NT rank tiles x k splits, splits fastest.
 template <bool BF16, int W, int NT>
 __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const LoraArgs p) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int NW = kShrinkWaves;
-  for_items<W>(p, p.splits * p.rank_blocks, [&](const Item& it, int part) {
-    const int split = part % p.splits, r0 = part / p.splits * (16 * NT);
-    if (r0 >= uniform(it.rank)) return;
-    const int key = uniform(it.key);
-    const uint64_t rows = (uint64_t)uniform((int64_t)it.rows);
-    const int64_t w0 = uniform(it.w0);
-    const int kb = split * p.kchunk, ke = min(p.k, kb + p.kchunk);
-    float* h = p.h + (int64_t)split * p.m * p.r;
-    if constexpr (W == 16) {
-      shrink_item<BF16, W, 1, NT, NW>(p, lds, w0, 0, key, rows, r0, kb, ke, h);
-    } else {
+  if constexpr (W == 16) {
+    // parts of an item: blocks of NT rank tiles x k splits, splits fastest
+    for_window(p, p.splits * p.rank_blocks, [&](const Item& it, int part) {
+      const int split = part % p.splits, r0 = part / p.splits * (16 * NT);
+      if (r0 >= uniform(it.rank)) return;
+      const int kb = split * p.kchunk, ke = min(p.k, kb + p.kchunk);
+      shrink_item<BF16, W, 1, NT, NW>(p, lds, uniform(it.w0), 0, uniform(it.key),
+                                      (uint64_t)uniform((int64_t)it.rows), r0, kb, ke, p.h + (int64_t)split * p.m * p.r);
+    });
+  } else {
+    const Lists lists(p);
+    const Shares shares(p, lists.items);
+    int64_t me = blockIdx.x;
+    if (me >= shares.n) return;
+    if ((shares.n & 7) == 0) me = (me & 7) * (shares.n >> 3) + (me >> 3);
+    const int64_t end = shares.begin(me + 1);
+    for (int64_t s = shares.begin(me); s < end;) {
+      const int64_t ir = s / p.steps;  // item x block of NT rank tiles
+      const int s0 = (int)(s - ir * p.steps), s1 = (int)min((int64_t)p.steps, s0 + (end - s));
+      s += s1 - s0;
+      const int64_t i = ir / p.rank_blocks;
+      const int r0 = (int)(ir - i * p.rank_blocks) * (16 * NT);
+      const Item it = p.items[lists.at(p, i)];
+      if (r0 >= uniform(it.rank)) continue;
+      float* h = p.h + (me - shares.of(ir * p.steps)) * p.m * p.r;  // this part's place
+      const int key = uniform(it.key), kb = 64 * s0, ke = min(p.k, 64 * s1);
+      const uint64_t rows = (uint64_t)uniform((int64_t)it.rows);
+      const int64_t w0 = uniform(it.w0);
       // rows inside one 16-row block (single tokens, the ends of prompts) read that block only
       const int lo = __builtin_ctzll(rows) >> 4, hi = (63 - __builtin_clzll(rows)) >> 4;
       if (lo == hi) shrink_item<BF16, W, 1, NT, NW>(p, lds, w0, lo, key, rows, r0, kb, ke, h);
       else shrink_item<BF16, W, 4, NT, NW>(p, lds, w0, 0, key, rows, r0, kb, ke, h);
     }
-  });
+  }
 }
 
 // ------------------------------------------------------------------------- out = x3 + h B^T
@@ -302,7 +336,7 @@ __device__ __forceinline__ uint32_t split_hi_lo(float v) {  // hi in bits 0-15, 
 constexpr int kSumRow = 36;  // floats of a row of 32 sums: rows 16 bytes apart in the banks
 __device__ __forceinline__ int column_turn(int n) { return ((n >> 1) & 1) | (((n >> 3) & 3) << 1); }
 
-// Parts of an item: blocks of p.cols columns.  A wave takes the window's rows (MT 16-row blocks) x 32
+// 16-row windows: parts of an item are blocks of p.cols columns.  A wave takes the window's rows (MT 16-row blocks) x 32
 // columns at a time, and the ranks in blocks of up to 8 CH.  Its sums go through LDS, 16 rows at a time,
 // so that four adjacent lanes read x3 and write the output in 64 bytes of a row.  Dynamic LDS: for
 // each wave two stages of B and 16 rows of sums, then W rows of hp = (r rounded up to 16) + 4
@@ -319,12 +353,12 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
   float* factor = (float*)(lds + W * hp);
   uint8_t* mine = stages + wave * 2 * Stage;
   const uint32_t to = lds_address(stages) + wave * 2 * Stage;
-  for_items<W>(p, p.col_blocks, [&](const Item& it, int part) {
+  // columns n_lo .. n1 - 1 of an item, whose h has parts_of(block of ranks) parts
+  auto expand_item = [&](const Item& it, int64_t n_lo, int64_t n1, const auto& parts_of) {
     const int key = uniform(it.key);
     const uint64_t rows = (uint64_t)uniform((int64_t)it.rows);
     const int64_t w0 = uniform(it.w0);
-    const int64_t n1 = min(p.n, ((int64_t)part + 1) * p.cols);
-    int64_t nc = (int64_t)part * p.cols + wave * 32;
+    int64_t nc = n_lo + wave * 32;
     const int rank = uniform(it.rank);
     if (rank == 0 && p.x3 == p.out) return;  // nothing to add in place
     const int nk = (rank + 15) / 16, steps = (rank + RB - 1) / RB;
@@ -372,27 +406,30 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
         }
         *(f32x4_t*)(lds + row * hp + c) = v;
       };
-      if (p.splits == 1) {
-        for (int c = first; c < 16 * nk; c += 16 * TPR) {  // four loads in flight
-          f32x4_t t[4];
+      for (int r0 = 0; r0 < (CH == 8 ? 16 * nk : 1); r0 += RB) {  // blocks of ranks of the first product
+        const int parts = parts_of(r0 / RB), r1 = min(16 * nk, r0 + RB);
+        if (parts == 1) {
+          for (int c = r0 + first; c < r1; c += 16 * TPR) {  // four loads in flight
+            f32x4_t t[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (have && c + 4 * TPR * i < rank) t[i] = *(const f32x4_t*)(hr + c + 4 * TPR * i);
+            for (int i = 0; i < 4; ++i)
+              if (have && c + 4 * TPR * i < rank) t[i] = *(const f32x4_t*)(hr + c + 4 * TPR * i);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c + 4 * TPR * i < 16 * nk) keep(t[i], c + 4 * TPR * i);
-        }
-      } else {
-        for (int c = first; c < 16 * nk; c += 4 * TPR) {
-          f32x4_t t[kLoraSplits], v = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          if (have && c < rank) {  // all splits in flight
-#pragma unroll
-            for (int z = 0; z < kLoraSplits; ++z) t[z] = *(const f32x4_t*)(hr + min(z, p.splits - 1) * step + c);
-#pragma unroll
-            for (int z = 0; z < kLoraSplits; ++z)
-              if (z < p.splits) v += t[z];
+            for (int i = 0; i < 4; ++i)
+              if (c + 4 * TPR * i < r1) keep(t[i], c + 4 * TPR * i);
           }
-          keep(v, c);
+        } else {
+          for (int c = r0 + first; c < r1; c += 4 * TPR) {
+            f32x4_t t[kLoraSplits], v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (have && c < rank) {  // all parts in flight
+#pragma unroll
+              for (int z = 0; z < kLoraSplits; ++z) t[z] = *(const f32x4_t*)(hr + min(z, parts - 1) * step + c);
+#pragma unroll
+              for (int z = 0; z < kLoraSplits; ++z)
+                if (z < parts) v += t[z];
+            }
+            keep(v, c);
+          }
         }
       }
 #pragma unroll
@@ -491,7 +528,25 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
         if (((rows >> wr) & 1) && nc + col4 < n1) *(u32x4_t*)(p.out + (w0 + wr) * p.so + nc + col4) = o[t];
       }
     }
-  });
+  };
+  if constexpr (W == 16) {
+    for_window(p, p.col_blocks, [&](const Item& it, int part) {
+      expand_item(it, (int64_t)part * p.cols, min(p.n, ((int64_t)part + 1) * p.cols), [&](int) { return p.splits; });
+    });
+  } else {
+    const Lists lists(p);
+    const Shares shares(p, lists.items);
+    const int64_t rounds = (p.n + kLoraCols - 1) / kLoraCols, total = lists.items * rounds;
+    const int64_t me = (int64_t)(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3), end = total * (me + 1) / gridDim.x;
+    for (int64_t u = total * me / gridDim.x; u < end;) {
+      const int64_t i = u / rounds, c0 = u - i * rounds, c1 = min(rounds, c0 + (end - u));
+      u += c1 - c0;
+      expand_item(p.items[lists.at(p, i)], c0 * kLoraCols, min(p.n, c1 * kLoraCols), [&](int rb) {
+        const int64_t s = (i * p.rank_blocks + rb) * p.steps;
+        return (int)(shares.of(s + p.steps - 1) - shares.of(s)) + 1;
+      });
+    }
+  }
 }
 
 // NT: 16-rank tiles of the first product's workgroups, and half the 16-byte chunks of a column of
@@ -533,6 +588,7 @@ hipError_t launch_lora(const LoraProblem& p, const LoraPlan& pl, void* workspace
   a.m = p.m; a.n = p.n; a.sx = p.sx; a.s3 = p.s3; a.so = p.so;
   a.k = p.k; a.r = p.r; a.L = (int32_t)p.L; a.splits = pl.splits; a.kchunk = pl.kchunk; a.slots = pl.slots; a.cols = pl.cols;
   a.windows = pl.windows; a.col_blocks = pl.col_blocks; a.rank_blocks = pl.rank_blocks;
+  a.steps = (p.k + 63) / 64; a.shrink_blocks = (int32_t)pl.shrink_blocks;
   static_assert(sizeof(Item) == kLoraItemBytes, "the plan's size of the list");
   const bool bf16 = p.act == WQ_BF16;
   if (pl.window == 16) return bf16 ? launch_ranks<true, 16>(a, pl, stream) : launch_ranks<false, 16>(a, pl, stream);

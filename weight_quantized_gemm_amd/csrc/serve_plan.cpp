@@ -27,7 +27,17 @@ LoraPlan plan_lora(const LoraProblem& p) {
   if (pl.window == 16) pl.slots = (int)std::min<int64_t>(distinct, p.m <= 64 ? 16 : 4);
   pl.rank_tiles = p.r <= 16 ? 1 : p.r <= 32 ? 2 : kLoraRankTiles;
   pl.rank_blocks = (int)ceil_div(p.r, 16 * pl.rank_tiles);
-  // k splits, a power of two (a split then stays on its XCDs), while workgroups are few
+  if (pl.window == 64) {  // as many workgroups as reside at once, both multiples of 8, share the steps
+    pl.shrink_blocks = kCUs;
+    pl.expand_blocks = 2 * kCUs;
+    pl.list_bytes = align256(4 * kLoraLists + (p.m + 2 * pl.windows) * kLoraItemBytes);
+    // parts of an item: its share is at least windows / kCUs items long, and never less than the least
+    // that keeps the parts within kLoraSplits
+    pl.splits = (int)std::min<int64_t>(kLoraSplits, kCUs / (pl.windows * pl.rank_blocks) + 2);
+    pl.workspace = align256(pl.list_bytes + (int64_t)pl.splits * p.m * p.r * 4);
+    return pl;
+  }
+  // k splits, a power of two, while workgroups are few
   const int64_t most = ceil_div(p.k, 256);
   while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && pl.windows * pl.rank_blocks * pl.splits < 2 * kCUs)
     pl.splits *= 2;
@@ -38,17 +48,10 @@ LoraPlan plan_lora(const LoraProblem& p) {
   const int64_t rounds = ceil_div(p.n, kLoraCols);
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(rounds, 4 * kCUs / (pl.windows * (p.m <= 64 ? pl.slots : 2))));
   pl.cols = (int)(ceil_div(rounds, blocks) * kLoraCols);
-  if (pl.window == 64) pl.cols = (int)std::min<int64_t>(rounds, 4) * kLoraCols;
   pl.col_blocks = (int)ceil_div(p.n, pl.cols);
-  if (pl.window == 16) {
-    pl.shrink_blocks = ceil_div(pl.windows * pl.slots * pl.rank_blocks * pl.splits, 8) * 8;
-    pl.expand_blocks = ceil_div(pl.windows * pl.slots * pl.col_blocks, 8) * 8;
-  } else {  // as many as reside at once walk the list; both multiples of 8
-    pl.shrink_blocks = kCUs;
-    pl.expand_blocks = 2 * kCUs;
-    pl.list_bytes = align256(4 * kLoraLists + (p.m + 2 * pl.windows) * kLoraItemBytes);
-  }
-  pl.workspace = align256(pl.list_bytes + (int64_t)pl.splits * p.m * p.r * 4);
+  pl.shrink_blocks = ceil_div(pl.windows * pl.slots * pl.rank_blocks * pl.splits, 8) * 8;
+  pl.expand_blocks = ceil_div(pl.windows * pl.slots * pl.col_blocks, 8) * 8;
+  pl.workspace = align256((int64_t)pl.splits * p.m * p.r * 4);
   return pl;
 }
 

@@ -339,6 +339,9 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
       for (int t = 0; t < NT; ++t) sc[t][h] = mfma16x16x32<BF16>(kf, w.q[t0 + t][j], sc[t][h]);
     }
 
+  // vector instructions first: the other wave of the SIMD is then sooner at its matrix products
+  // (512 rows: 243 -> 238 us)
+  if constexpr (!SLOW) __builtin_amdgcn_s_setprio(1);
   uint32_t seen[NT][KT / 32];  // SLOW: bit r of word b, whether this lane's row sees key 32 b + r
   if constexpr (SLOW) {
 #pragma unroll
@@ -390,9 +393,13 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
   }
   if constexpr (!SLOW) {
     constexpr uint16_t kMost = BF16 ? (127 + kSlack) << 7 : (15 + kSlack) << 10;
-    if (__ballot(most[0] > kMost || most[1] > kMost)) return false;
+    if (__ballot(most[0] > kMost || most[1] > kMost)) {
+      __builtin_amdgcn_s_setprio(0);
+      return false;
+    }
   }
 
+  if constexpr (!SLOW) __builtin_amdgcn_s_setprio(0);
   constexpr uint32_t kOne2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
