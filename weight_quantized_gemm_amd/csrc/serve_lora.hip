@@ -278,7 +278,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const Lo
     // parts of an item: blocks of NT rank tiles x k splits, splits fastest
     for_window(p, p.splits * p.rank_blocks, [&](const Item& it, int part) {
       const int split = part % p.splits, r0 = part / p.splits * (16 * NT);
-      if (r0 >= uniform(it.rank)) return;
+      // rows without an adapter; ranks past the adapter's (the first block does not wait for the rank)
+      if (uniform(it.key) < 0 || (r0 > 0 && r0 >= uniform(it.rank))) return;
       const int kb = split * p.kchunk, ke = min(p.k, kb + p.kchunk);
       shrink_item<BF16, W, 1, NT, NW>(p, lds, uniform(it.w0), 0, uniform(it.key),
                                       (uint64_t)uniform((int64_t)it.rows), r0, kb, ke, p.h + (int64_t)split * p.m * p.r);
@@ -359,9 +360,7 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
     const uint64_t rows = (uint64_t)uniform((int64_t)it.rows);
     const int64_t w0 = uniform(it.w0);
     int64_t nc = n_lo + wave * 32;
-    const int rank = uniform(it.rank);
-    if (rank == 0 && p.x3 == p.out) return;  // nothing to add in place
-    const int nk = (rank + 15) / 16, steps = (rank + RB - 1) / RB;
+    if (key < 0 && p.x3 == p.out) return;  // nothing to add in place
 
     // Loads take any row or column of the tensors where theirs are past the end (what comes of it is not
     // stored, or is cleared below): without a condition they all go out at once.
@@ -386,9 +385,10 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
     const bool busy = nc < n1;
     if (busy) {  // on their way while h is made ready
       load_x(nc);
-      if (rank) load_b(nc, 0, to);
+      if (key >= 0) load_b(nc, 0, to);
     }
 
+    const int rank = uniform(it.rank), nk = (rank + 15) / 16, steps = (rank + RB - 1) / RB;
     if (rank) {  // h of the adapter's rows: splits added in order, scaled, split into hi + lo
       __syncthreads();
       constexpr int TPR = 256 / W;  // threads of a row, four ranks each at a time
@@ -528,6 +528,7 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
         if (((rows >> wr) & 1) && nc + col4 < n1) *(u32x4_t*)(p.out + (w0 + wr) * p.so + nc + col4) = o[t];
       }
     }
+    if (rank == 0) wave_wait<0>();  // B was asked for; no load into the LDS is left
   };
   if constexpr (W == 16) {
     for_window(p, p.col_blocks, [&](const Item& it, int part) {

@@ -39,8 +39,8 @@ LoraPlan plan_lora(const LoraProblem& p) {
   }
   // k splits, a power of two, while workgroups are few
   const int64_t most = ceil_div(p.k, 256);
-  while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && pl.windows * pl.rank_blocks * pl.splits < 2 * kCUs)
-    pl.splits *= 2;
+  const int64_t items = pl.windows * (p.m <= 64 ? std::min<int64_t>(4, pl.slots) : 2) * pl.rank_blocks;
+  while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && 2 * items * pl.splits <= 2 * kCUs) pl.splits *= 2;
   pl.kchunk = (int)(ceil_div(ceil_div(p.k, pl.splits), 64) * 64);
   pl.splits = (int)ceil_div(p.k, pl.kchunk);
   // second product: workgroups of whole rounds of columns, as many as reside at once if a larger

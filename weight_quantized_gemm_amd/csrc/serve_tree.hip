@@ -74,7 +74,6 @@ struct TreeArgs {
   uint32_t q_and, q_xor;
 };
 
-constexpr int kSlots = 1024;    // keys whose slots stand in LDS at a time
 constexpr int kSlack = 8;       // log2 of the largest weight
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 constexpr float kNone = -__builtin_inff();
@@ -215,7 +214,7 @@ __device__ __forceinline__ bool not_finite(uint32_t half) {
 // Bit r: whether key r of the tile exists.
 template <int KT>
 __device__ __forceinline__ uint64_t tile_keys(const int* slots, int first, int lane) {
-  return __ballot(lane < KT && slots[min(first + lane, kSlots - 1)] >= 0);
+  return __ballot(lane < KT && slots[first + (lane & (KT - 1))] >= 0);
 }
 
 // Part `w` of `parts` of V without what the product must not meet; returns the rows (bits) of this
@@ -560,7 +559,8 @@ struct KeysLds {
   static constexpr int NW = tree_key_waves(HD), R = 16 * RT, Pad = HD + 4;  // Pad: floats of a joining row
   // the waves' stages, later their rows
   static constexpr int Area = std::max(NW * 2 * Cfg<HD, 32>::Stage, NW * R * Pad * 4);
-  static constexpr int Total = Area + kSlots * 4 + NW * R * 8;  // slots, (base, sum) of each wave's rows
+  static constexpr int Slots = HD == 64 ? 2048 : 4096;          // keys whose slots stand in LDS at a time
+  static constexpr int Total = Area + Slots * 4 + NW * R * 8;  // slots, (base, sum) of each wave's rows
 };
 
 template <int HD, bool BF16, int RT>
@@ -570,7 +570,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
   constexpr int R = L::R, NW = L::NW;
   extern __shared__ __align__(16) uint8_t lds[];
   int* slots = (int*)(lds + L::Area);
-  float* stat = (float*)(lds + L::Area + kSlots * 4);
+  float* stat = (float*)(lds + L::Area + L::Slots * 4);
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int64_t total, me, u, u_end;
@@ -586,8 +586,8 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
 
     uint8_t* mine = lds + wave * 2 * C::Stage;
     const uint32_t to = lds_address(lds) + wave * 2 * C::Stage;
-    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += kSlots) {
-      const int count = min(kSlots, p.key_hi - key0);
+    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += L::Slots) {
+      const int count = min(L::Slots, p.key_hi - key0);
       __syncthreads();  // the slots (and the joining rows in the stages) have been read
       const int lost = uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
       const int tiles = (count + 31) / 32;
@@ -692,7 +692,8 @@ template <int HD, int NW>
 struct RowsLds {
   static constexpr int KT = tree_row_keys(NW);
   static constexpr int Area = 2 * Cfg<HD, KT>::Stage;
-  static constexpr int Total = Area + kSlots * 4 + NW * 8;  // slots, each wave's odd rows
+  static constexpr int Slots = 512 * NW;                   // keys whose slots stand in LDS at a time
+  static constexpr int Total = Area + Slots * 4 + NW * 8;  // slots, each wave's odd rows
 };
 
 template <int HD, bool BF16, int NW>
@@ -701,7 +702,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
   using C = Cfg<HD, KT>;
   extern __shared__ __align__(16) uint8_t lds[];
   int* slots = (int*)(lds + RowsLds<HD, NW>::Area);
-  uint64_t* odd_of = (uint64_t*)(slots + kSlots);
+  uint64_t* odd_of = (uint64_t*)(slots + RowsLds<HD, NW>::Slots);
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int64_t total, me, u, u_end;
@@ -715,8 +716,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
     const int row0 = p.row0 + 16 * RT * wave;
     Rows<HD, RT> w;
     start_rows<HD, BF16, RT>(a, p.s, p.kvh, row0, p.rows, lane, w);
-    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += kSlots) {
-      const int count = min(kSlots, p.key_hi - key0);
+    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += RowsLds<HD, NW>::Slots) {
+      const int count = min(RowsLds<HD, NW>::Slots, p.key_hi - key0);
       __syncthreads();  // the slots and stages have been read
       const int lost = uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
       const int tiles = (count + KT - 1) / KT;
