@@ -108,7 +108,11 @@ LORA = [  # m, L, r, k, n, order, ranks, scale, x3
     (1024, 1, 8, 72, 1000, "one", False, True, False),
     (1025, 5, 64, 1032, 520, "runs", True, True, True),
     (1100, 200, 40, 128, 264, "mixed", True, True, True),
+    (2049, 5, 64, 1032, 520, "runs", True, True, True),
+    (2100, 200, 40, 128, 264, "mixed", True, True, True),
+    (2111, 3, 16, 72, 136, "mixed", True, False, False),
     (4099, 6, 256, 512, 256, "runs", False, True, True),
+    (20000, 4, 24, 4104, 72, "runs", True, True, True),
 ]
 
 
@@ -125,7 +129,7 @@ def test_lora(case, dt):
 
 def test_lora_indices_out_of_range_and_none():
     say("lora no adapters")
-    for m in (5, 1500):
+    for m in (5, 1500, 2500):
         c = lora_case(3, torch.bfloat16, m, 3, 16, 64, 72)
         c["indices"] = torch.tensor([-1, 3, 2 ** 31 - 1, -2 ** 31, 7], dtype=torch.int32, device=DEV).repeat(m // 5)
         assert torch.equal(lora_run(c), c["x3"])
@@ -138,7 +142,7 @@ def test_lora_past_the_rank_and_other_rows_do_not_matter():
     infinities in a neighbour's row leave a row's bits as they are."""
     say("lora isolation")
     for dt in DTYPES:
-        for m in (37, 1200):
+        for m in (37, 1200, 2200):
             c = lora_case(11, dt, m, 6, 40, 264, 136, order="mixed")
             c["ranks"] = torch.tensor([0, 3, 8, 21, 39, 40], dtype=torch.int32, device=DEV)
             c["indices"] = torch.where(c["indices"] == 4, -1, c["indices"]).int()
@@ -171,7 +175,7 @@ def test_lora_first_product_beyond_fp16():
 def test_lora_strides_in_place_and_shapes():
     say("lora strides")
     dt = torch.bfloat16
-    for m in (20, 1030):
+    for m in (20, 1030, 2060):
         c = lora_case(7, dt, m, 4, 24, 136, 72, order="mixed", ranks=True)
         ref, bound = lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], c["ranks"], c["x3"])
         wide_x = torch.full((m, 136 + 24), float("nan"), dtype=dt, device=DEV)

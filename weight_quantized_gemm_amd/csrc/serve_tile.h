@@ -6,7 +6,7 @@
 namespace wq {
 
 // ---- adapters
-constexpr int64_t kLoraSmallM = 1024;  // up to here a window is 16 token rows, beyond 64
+constexpr int64_t kLoraSmallM = 2048;  // up to here a window is 16 token rows, beyond 64
 constexpr int kLoraRankTiles = 4;      // most 16-rank tiles of one workgroup of the first product
 constexpr int kLoraCols = 128;         // columns of one round of the second product's workgroups
 constexpr int kLoraSplits = 8;         // most k splits of the first product
