@@ -32,9 +32,11 @@
 // 2^kSlack, which fp32 and both 16-bit types hold; a tile whose weights pass that is taken again,
 // with its maximum found, the base raised and the outputs rescaled.  Most tiles thus find no
 // maximum at all, which costs as many vector instructions as the weights themselves.  The
-// weights are rounded to 16 bits for the second product: an error of at most 2^-8 (bf16) or
-// 2^-11 (fp16) of each, of the size of the result's own rounding.  Their sums are taken of the
-// rounded weights, by the matrix cores (against ones), so that the weights add up to 1 exactly.
+// weights are rounded to 16 bits for the second product.  The keys kernel, whose matrix cores wait for
+// memory anyway, takes what the rounding left as a second 16-bit term, and is as exact as fp32
+// weights; the rows kernel does not, for an error of at most 2^-8 (bf16) or 2^-11 (fp16) of each
+// weight, of the size of the result's own rounding.  The sums are taken of the rounded weights,
+// by the matrix cores (against ones), so that the weights add up to 1 exactly.
 #include <algorithm>
 #include <cmath>
 
@@ -307,7 +309,7 @@ __device__ __forceinline__ void start_rows(const TreeArgs& a, const Seq& s, int 
 // and the rows `odd` of V that clean_values took infinities or NaN from.  Otherwise all keys are seen and
 // the bases stay; returns false, with nothing summed, where a row has no base yet or a weight
 // passes 2^kSlack.
-template <int HD, bool BF16, int RT, int NT, int KT, bool SLOW>
+template <int HD, bool BF16, int RT, int NT, int KT, bool SLOW, bool TWO>
 __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
                                              uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
                                              int lane, const int t0, Rows<HD, RT>& w) {
@@ -368,7 +370,7 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
     }
   }
 
-  u32x4_t pf[NT][KT / 32];
+  u32x4_t pf[NT][KT / 32], pl[NT][KT / 32];  // TWO: pl, what the rounding of pf left
   u16x2_t most = {0, 0};  // of the weights' bits, which order like the weights (a NaN is above all)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -382,6 +384,13 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
       pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
                          pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
                          pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
+      if constexpr (TWO)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p0 = sc[t][2 * b + e / 2][2 * (e & 1)], p1 = sc[t][2 * b + e / 2][2 * (e & 1) + 1];
+          pl[t][b][e] = pack2<BF16>(p0 - act_to_f32<BF16>((uint16_t)pf[t][b][e]),
+                                    p1 - act_to_f32<BF16>((uint16_t)(pf[t][b][e] >> 16)));
+        }
       asm volatile("" : "+v"(pf[t][b]));  // rounded once: it is not made again for the product
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -404,7 +413,10 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int b = 0; b < KT / 32; ++b)
+    {
       w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pf[t][b], w.l[t0 + t]);
+      if constexpr (TWO) w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pl[t][b], w.l[t0 + t]);
+    }
 
   // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3 of each 32; rows 16 apart and columns 16
   // apart as above
@@ -418,7 +430,10 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
       const u32x2_t hi = lds_read_tr16(vs + (v0 ^ (32 * d)) + (32 * b + 16) * C::RB);
       const u32x4_t vf = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t0 + t][d]);
+      for (int t = 0; t < NT; ++t) {
+        w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t0 + t][d]);
+        if constexpr (TWO) w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pl[t][b], w.o[t0 + t][d]);
+      }
     }
 
   if constexpr (SLOW) {
@@ -454,14 +469,14 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
 }
 
 // All of a wave's row blocks: at once, where that will do (false: nothing was done) ...
-template <int HD, bool BF16, int RT, int KT>
+template <int HD, bool BF16, int RT, int KT, bool TWO>
 __device__ __forceinline__ bool compute_fast(const TreeArgs& a, const uint8_t* stage, int lane, Rows<HD, RT>& w) {
-  return compute_rows<HD, BF16, RT, RT, KT, false>(a, Seq{}, nullptr, 0, 0, 0, 0, stage, nullptr, lane, 0, w);
+  return compute_rows<HD, BF16, RT, RT, KT, false, TWO>(a, Seq{}, nullptr, 0, 0, 0, 0, stage, nullptr, lane, 0, w);
 }
 // ... or one by one, which takes fewer registers.  The loops over tiles below keep to the first form
 // and leave for the second: in one loop with both, the outputs would change registers at every
 // tile (40 moves).
-template <int HD, bool BF16, int RT, int KT>
+template <int HD, bool BF16, int RT, int KT, bool TWO>
 __device__ __forceinline__ void compute_slow(const TreeArgs& a, const Seq& s, const int* slots, int first, bool edge,
                                              int draft0, uint64_t keys, uint64_t odd, const uint8_t* stage,
                                              const uint16_t* vh, int lane, Rows<HD, RT>& w) {
@@ -472,7 +487,7 @@ __device__ __forceinline__ void compute_slow(const TreeArgs& a, const Seq& s, co
   }
 #pragma unroll
   for (int t = 0; t < RT; ++t)
-    compute_rows<HD, BF16, RT, 1, KT, true>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
+    compute_rows<HD, BF16, RT, 1, KT, true, TWO>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
 }
 
 // 1 / sum; no key seen: 0; NaN stays
@@ -615,7 +630,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
         bool edge = false;
         for (; j < tiles; end()) {
           edge = begin();
-          if (edge || !compute_fast<HD, BF16, RT, 32>(a, mine + st * C::Stage, lane, w)) break;
+          if (edge || !compute_fast<HD, BF16, RT, 32, true>(a, mine + st * C::Stage, lane, w)) break;
         }
         if (j >= tiles) break;
         uint8_t* stage = mine + st * C::Stage;
@@ -625,7 +640,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
           odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
           __builtin_amdgcn_wave_barrier();
         }
-        compute_slow<HD, BF16, RT, 32>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+        compute_slow<HD, BF16, RT, 32, true>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
         end();
       }
     }
@@ -736,7 +751,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
           if (j + 1 < tiles)
             load_tile<HD, KT, NW>(a, kh, vh, slots, KT * (j + 1), to + ((j + 1) & 1) * C::Stage, wave, lane);
           edge = lost || KT * (j + 1) > count || key0 + KT * (j + 1) - p.s.ctx > 0;
-          if (edge || !compute_fast<HD, BF16, RT, KT>(a, lds + (j & 1) * C::Stage, lane, w)) break;
+          if (edge || !compute_fast<HD, BF16, RT, KT, false>(a, lds + (j & 1) * C::Stage, lane, w)) break;
         }
         if (j >= tiles) break;
         uint8_t* stage = lds + (j & 1) * C::Stage;
@@ -749,7 +764,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
 #pragma unroll
           for (int i = 0; i < NW; ++i) odd |= odd_of[i];
         }
-        compute_slow<HD, BF16, RT, KT>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+        compute_slow<HD, BF16, RT, KT, false>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
         ++j;
       }
     }
