@@ -49,7 +49,8 @@ extern "C" {
  *            Absent means 0.  It may be the output itself (same address and strides).
  *   output   required; x1's dtype; rows (m, n) or (b, s, n) following x1.
  * m == 0 is a call with nothing to do.  Both products are summed in fp32; the result is
- * rounded once.  Results do not depend on the other tokens of the call.
+ * rounded once.  A token's result takes nothing from the other tokens' values,
+ * and equal calls give equal bits.
  */
 int wq_lora_matmul_get_workspace_size(const wq_tensor* x1, const wq_tensor* a, const wq_tensor* b,
                                       const wq_tensor* indices, const wq_tensor* scale,
@@ -121,7 +122,8 @@ int wq_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq
  *   scale         finite.
  *   output        required; q's dtype; rows (N, hq, d), not overlapping an input.
  * N == 0 or B == 0 is a call with nothing to do.  Scores, the softmax and the sums are fp32;
- * the weights p are rounded to q's dtype for the product with v.
+ * the weights p go into the product with v as one number of q's dtype, or, where the average
+ * sequence has at most 32 rows (tokens x query heads of a cached head) or d = 256, as the sum of two.
  */
 int wq_tree_attention_get_workspace_size(const wq_tensor* q, const wq_tensor* k_cache,
                                          const wq_tensor* v_cache, const wq_tensor* block_table,

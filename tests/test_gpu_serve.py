@@ -160,6 +160,18 @@ def test_lora_past_the_rank_and_other_rows_do_not_matter():
             assert torch.equal(y[keep], clean[keep]) and not torch.isfinite(y[bad]).all()
 
 
+def test_lora_equal_calls_give_equal_bits():
+    """Mixed adapters in more windows than there are lists of work items."""
+    say("lora repeats")
+    for m, L, r, k, n in [(9001, 12, 16, 1024, 136), (4099, 64, 64, 512, 72), (700, 8, 32, 4096, 264)]:
+        c = lora_case(17, torch.bfloat16, m, L, r, k, n, order="mixed")
+        first = lora_run(c)
+        for _ in range(8):
+            assert torch.equal(lora_run(c), first), m
+        ref, bound = lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], None, c["x3"])
+        close(first, ref, bound, m)
+
+
 def test_lora_first_product_beyond_fp16():
     """h passes fp16's range while the result is back inside it."""
     say("lora large h")

@@ -25,6 +25,16 @@
 //    from there into the matrix cores' layout.  Loaded from memory in that layout, where lanes
 //    that follow each other hold different rows, every lane is an access of its own: 389 us
 //    instead of 125 us without the loads of B, for 16384 tokens x 8192 columns at rank 64.
+//
+// Measured (bf16, MI355X, a call with both products):
+//   1 token, rank 16, k = n = 4096: 8.5 us, of which the kernels take 3.0 and 4.7 us: two launches
+//     and the chain index -> rank -> operands -> sum in each;
+//   64 tokens of 32 adapters, rank 32, k = n = 8192 (fp16): 18.5 us for 26.8 MB, kernels 8.4 and
+//     11.4 us (1.0 and 1.6 TB/s): a workgroup lives for four rounds of loads and its launch and
+//     start take as long as those;
+//   16384 tokens of 8 adapters, rank 64, k = 4096, n = 8192: 201 us for 669 MB (3.3 TB/s; a copy runs at
+//     5.2); 5 us the list, 51 us the first product (2.6 TB/s of x1), 144 us the second (3.7 TB/s: x3
+//     and out through LDS, between loads of B that stand in the same queue).
 #include <algorithm>
 
 #include "serve_device.h"
@@ -80,27 +90,37 @@ __device__ __forceinline__ Item make_item(const LoraArgs& p, int64_t w0, int key
 }
 
 // The items of 64-row windows.  The first item of window w is items[w]; the others of the windows of
-// workgroup i of this kernel stand from items[windows + its first row] on, count[i] of them, in any
-// order (items do not depend on each other).
+// workgroup i of this kernel stand from items[windows + its first row] on, count[i] of them, in the order
+// of the windows.  The order is part of the result: the shares cut an item's sum where it stands.
 __global__ __launch_bounds__(256) void lora_items_kernel(const LoraArgs p) {
-  __shared__ int32_t more;
+  __shared__ int32_t found[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (threadIdx.x == 0) more = 0;
-  __syncthreads();
   const int64_t share = (p.windows + kLoraLists - 1) / kLoraLists, lo = blockIdx.x * share;
   const int64_t hi = min(p.windows, lo + share);
-  for (int64_t w = lo + wave; w < hi; w += 4) {
-    const int mine = lane_key<64>(p, w * 64, lane);
-    uint64_t left = __ballot(mine >= -1);
-    for (int s = 0; left; ++s) {
-      const int key = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-      const uint64_t rows = __ballot(mine == key);
+  int total = 0;
+  for (int64_t w4 = lo; w4 < hi; w4 += 4) {  // a window for each wave
+    const int64_t w = w4 + wave;
+    const int mine = w < hi ? lane_key<64>(p, w * 64, lane) : -2;
+    int keys = 0, nth = -1;  // of the window; the key whose first row is this lane's, or -1
+    uint64_t its_rows = 0;
+    for (uint64_t left = __ballot(mine >= -1); left; ++keys) {
+      const int first = __builtin_ctzll(left);
+      const uint64_t rows = __ballot(mine == __builtin_amdgcn_readlane(mine, first));
       left &= ~rows;
-      if (lane == 0) p.items[s == 0 ? w : p.windows + lo * 64 + atomicAdd(&more, 1)] = make_item(p, w * 64, key, rows);
+      if (lane == first) nth = keys, its_rows = rows;
     }
+    if (lane == 0) found[wave] = max(keys - 1, 0);
+    __syncthreads();
+    int64_t at = p.windows + lo * 64 + total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < wave) at += found[i];
+      total += found[i];
+    }
+    if (nth >= 0) p.items[nth == 0 ? w : at + nth - 1] = make_item(p, w * 64, mine, its_rows);
+    __syncthreads();
   }
-  __syncthreads();
-  if (threadIdx.x == 0) p.count[blockIdx.x] = more;
+  if (threadIdx.x == 0) p.count[blockIdx.x] = total;
 }
 
 // 16-row windows: calls body(item, part) for this workgroup's items, `parts` workgroups to an item, parts

@@ -22,7 +22,11 @@ LoraPlan plan_lora(const LoraProblem& p) {
   pl.window = p.m <= kLoraSmallM ? 16 : 64;
   pl.windows = ceil_div(p.m, pl.window);
   // Side-by-side work items of a 16-row window, whose rows may each have an adapter of their own:
-  // all of them where there are few windows, otherwise 4 (most workgroups of more would find nothing).
+  // all of them where there are few windows, otherwise 4, since most workgroups of more would find
+  // nothing.  16 against 4 of them: 13.1 us and 19.7 us for 64 tokens of 64 adapters (rank 16, k = n =
+  // 4096), 26.4 us and 22.5 us for 128 tokens of 64, 45 us and 36 us for 777 tokens of 100 requests.
+  // Only where most rows of many windows differ does that rule lose (1500 tokens of 1500 requests
+  // and 32 adapters: 83 us and 91 us), which the shapes do not tell.
   const int64_t distinct = std::min<int64_t>({p.L + 1, p.m, pl.window});
   if (pl.window == 16) pl.slots = (int)std::min<int64_t>(distinct, p.m <= 64 ? 16 : 4);
   pl.rank_tiles = p.r <= 16 ? 1 : p.r <= 32 ? 2 : kLoraRankTiles;
@@ -37,7 +41,9 @@ LoraPlan plan_lora(const LoraProblem& p) {
     pl.workspace = align256(pl.list_bytes + (int64_t)pl.splits * p.m * p.r * 4);
     return pl;
   }
-  // k splits, a power of two, while workgroups are few
+  // k splits, a power of two, while workgroups are few: 4 of 64 tokens' windows, 2 of more, are
+  // counted for a window.  (All of them split in 8 instead: 13.2 us for 13.0 us at 64 tokens of 64
+  // adapters, 38.0 us for 36.4 us at 777 of 100 requests.)
   const int64_t most = ceil_div(p.k, 256);
   const int64_t items = pl.windows * (p.m <= 64 ? std::min<int64_t>(4, pl.slots) : 2) * pl.rank_blocks;
   while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && 2 * items * pl.splits <= 2 * kCUs) pl.splits *= 2;
@@ -58,8 +64,17 @@ LoraPlan plan_lora(const LoraProblem& p) {
 TreePlan plan_tree(const TreeProblem& p) {
   TreePlan pl;
   if (p.N == 0 || p.B == 0) return pl;
-  // Rows of the average sequence: a tile of too many rows only pads, one of too few reads the
-  // keys again.
+  // Rows (tokens x heads that share a cached head) of the average sequence: a tile of too many rows
+  // only pads, one of too few reads the keys again.  bf16, d = 128, 8 cached heads, 8192 keys:
+  //   16 rows, 32 sequences: tiles of 16 rows 195 us, of 32 200 us
+  //   20 rows, 32 sequences: tiles of 16 rows 374 us, of 32 201 us
+  //   32 rows, 32 sequences: waves that split the keys 205 us, that split the rows (64) 210 us
+  //   48 rows, 16 sequences: waves that split the keys 134 us, that split the rows (64) 124 us
+  //   64 rows, 16 sequences: 2 waves 127 us, 4 125 us;  48 rows of 4 cached heads: 70 us, 74 us
+  //   112 rows, 16 sequences: 2 waves 138 us, 4 130 us, 8 180 us
+  //   256 rows, 16 sequences: 4 waves 195 us, 8 186 us;  512 rows, 8 sequences: 182 us, 172 us
+  // At d = 256 the outputs of a wave of more than 16 rows, or any of the other kernel, would not
+  // fit its registers.
   const int64_t rows = ceil_div(p.N, std::min(p.N, p.B)) * p.group;
   int per_cu = 1;  // workgroups that a compute unit holds: by LDS, and 8 waves of 256 registers
   if (rows <= 32 || p.d == 256) {

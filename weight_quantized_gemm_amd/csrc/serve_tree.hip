@@ -37,6 +37,18 @@
 // weights; the rows kernel does not, for an error of at most 2^-8 (bf16) or 2^-11 (fp16) of each
 // weight, of the size of the result's own rounding.  The sums are taken of the rounded weights,
 // by the matrix cores (against ones), so that the weights add up to 1 exactly.
+//
+// Measured (MI355X, both kernels of a call):
+//   64 single tokens over 16 to 8192 keys, 8 cached heads of 128, fp16: 248 us for 1.36 GB, 5.5 TB/s; reads
+//     of 256-byte pieces 2 KB apart, which a cache of 8 heads is made of, reach 6.1 TB/s with no
+//     arithmetic at all;
+//   one token over 4020 keys (4.1 MB): 12.7 us, 9.3 + 3.1 us in the kernels: launches and the chain
+//     length -> page -> key -> score -> join;
+//   8 sequences of 64 drafted tokens, 64 query heads for 8 cached ones of 128, bf16: 236 us,
+//     765 TFLOP/s of the 1215 that a large product reaches.  The matrix cores are busy for 37 % of
+//     the cycles, the vector units for 41 % (exponentials, packing, addresses), LDS for 19 %
+//     without bank conflicts: what is lost is that the two waves of a SIMD, held together by the
+//     shared tiles, do the same thing at the same time.
 #include <algorithm>
 #include <cmath>
 
