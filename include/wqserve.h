@@ -110,11 +110,11 @@ int wq_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq
  *   k_cache       required; q's dtype; rows (S, hkv, d); S a multiple of page_size, at most
  *                 2^31-1; its row stride at most 2^30; hq a multiple of hkv.
  *   v_cache       required; q's dtype; rows (S, hkv, d), like k_cache.
- *   block_table   required; WQ_I32; (B, W), contiguous; W * page_size at most 2^31-1.  Keys past
+ *   block_table   required; WQ_I32; (B, W), contiguous; W * page_size at most 2^31-2^16.  Keys past
  *                 its width, and keys on a page outside [0, S / page_size), are not seen.
  *   context_lens  required; WQ_I32; (B); a negative length counts as 0.
  *   q_starts      required; WQ_I32; (B + 1), ascending, clamped to [0, N].  Rows of output that
- *                 no sequence has are not written.
+ *                 no sequence has are not written (nor, if starts do not ascend, need others be).
  *   tree_mask     optional; WQ_I32; (N, words): bit j % 32 of word j / 32 of a token's row says
  *                 whether it sees token j of its sequence; tokens past 32 * words are not seen.
  *                 Absent: each token sees the tokens of its sequence up to itself.

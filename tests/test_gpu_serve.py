@@ -494,6 +494,24 @@ def test_tree_scores_that_jump(dt, hq, tokens):
     close(tree_run(c), ref, bound, "ramp")
 
 
+def test_tree_starts_that_do_not_ascend():
+    """More row tiles than ascending starts can make: nothing is written outside the output and the
+    workspace, and the next call is right."""
+    say("tree starts")
+    for tokens, hq in ((64, 8), (2, 8)):
+        c = tree_case(31, torch.bfloat16, [(70, tokens)] + [(40, 0)] * 7, hq, 2, 64, 16, mask=None)
+        call = W.TreeAttention(c["q"], c["k"], c["v"], c["table"], c["context"], c["starts"], page_size=16)
+        size = call.workspace_size
+        ws = torch.full((size + (1 << 20),), 90, dtype=torch.uint8, device=DEV)
+        good = tree_run(c, workspace=ws).clone()
+        ref, bound = tree_ref(c)
+        close(good, ref, bound, tokens)
+        odd = dict(c, starts=torch.tensor([0, tokens] * 4 + [0], dtype=torch.int32, device=DEV))
+        tree_run(odd, workspace=ws)
+        assert (ws[size:] == 90).all()
+        assert torch.equal(tree_run(c, workspace=ws), good)
+
+
 def test_tree_strides():
     """q as a slice of a projection, K and V interleaved in one cache, output heads first."""
     say("tree strides")

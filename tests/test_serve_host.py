@@ -206,6 +206,13 @@ def test_tree_accepts(wqlib):
         assert st == OK and size <= (66 << 20) + 2 * kw["N"]
 
 
+def test_tree_longest_tables(wqlib):
+    assert tree(wqlib, **tree_args(page=1 << 16, width=32767, pages=4))[0] == OK
+    assert tree(wqlib, **tree_args(page=1 << 15, width=65535, pages=4)) == INVALID
+    assert tree(wqlib, **tree_args(page=1, width=(1 << 31) - 65535, pages=4)) == INVALID
+    assert tree(wqlib, **tree_args(page=1, width=(1 << 31) - 65536, pages=4))[0] == OK
+
+
 def test_tree_refuses(wqlib):
     for name in ("q", "k_cache", "v_cache", "block_table", "context_lens", "q_starts", "output"):
         assert tree(wqlib, **{name: None}) == NULLPTR, name

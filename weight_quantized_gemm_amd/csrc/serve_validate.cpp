@@ -281,7 +281,8 @@ int validate_tree(const wq_tensor* q, const wq_tensor* k_cache, const wq_tensor*
   if (N > (1 << 24) || N * hq > (1 << 30) || B > 65535) return WQ_ERR_PARAM_INVALID;
   if (k_cache->shape[2] != d || S % page_size != 0 || !same_shape(k_cache, v_cache) || !same_shape(q, output))
     return WQ_ERR_PARAM_INVALID;
-  if (width * page_size > kMaxExtent) return WQ_ERR_PARAM_INVALID;
+  // keys past the last by a tile, a unit or the slots that stand in LDS are still 32-bit numbers
+  if (width * page_size > kMaxExtent - 65535) return WQ_ERR_PARAM_INVALID;
   if (context_lens->shape[0] != B || q_starts->shape[0] != B + 1) return WQ_ERR_PARAM_INVALID;
   if (tree_mask && (tree_mask->shape[0] != N || tree_mask->shape[1] > (1 << 20))) return WQ_ERR_PARAM_INVALID;
 
