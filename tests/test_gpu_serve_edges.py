@@ -1,0 +1,27 @@
+"""The serving operators where variants, tiles and types meet their ends (GPU); references and bounds are those
+of test_gpu_serve.py."""
+import pytest
+import torch
+
+import test_gpu_serve as base
+import weight_quantized_gemm_amd as W
+
+pytestmark = pytest.mark.gpu
+
+DEV, DTYPES = base.DEV, base.DTYPES
+say, close, gen, rnd = base.say, base.close, base.gen, base.rnd
+tree_case, tree_run, tree_ref = base.tree_case, base.tree_run, base.tree_ref
+IDS = ["bf16", "fp16"]
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (14, 2, 64), (4, 1, 128), (8, 2, 256)])
+def test_tree_long_sequences_among_short_ones(hq, hkv, d, dt):
+    """One sequence of several tiles whose height its neighbours' single tokens chose, each tile's keys shared by
+    several workgroups: every row is joined from its own tile's parts."""
+    say("tree uneven", hq, hkv, d, dt)
+    c = tree_case(91, dt, [(300, 5), (310, 1), (290, 1), (305, 1), (297, 1)], hq, hkv, d, 16, None)
+    ref, bound = tree_ref(c)
+    for _ in range(5):
+        out = torch.full_like(c["q"], 9.0)
+        close(tree_run(c, out=out), ref, bound, (hq, hkv, d))

@@ -831,7 +831,7 @@ __global__ __launch_bounds__(256) void tree_join_kernel(const TreeArgs a) {
     if (cut.parts == 0) continue;
     // part 0 is the first workgroup's second, part i the first of the workgroup i places on
     auto place = [&](int i) { return ((int64_t)2 * (cut.first + i) + (i == 0 ? 1 : 0)) * a.R + row; };
-    const bool live = cut.row0 + row < cut.rows;
+    const bool live = row < a.R && cut.row0 + row < cut.rows;  // (at d = 64 a block may be two tiles' rows high)
     float base = kNone, sum = 0.f;
     f32x4_t y0 = f32x4_t{0.f, 0.f, 0.f, 0.f}, y1 = y0;
     for (int i0 = SPLIT ? wave : 0; live && i0 < cut.parts; i0 += U * step) {
