@@ -1,0 +1,31 @@
+"""Host side of the serving operators at the ends of their ranges (CPU)."""
+import math
+
+import pytest
+
+import weight_quantized_gemm_amd as W
+
+
+@pytest.mark.parametrize("rot,base,length,factor", [(128, 1e4, 131072, 8.0), (64, 1e4, 65536, 4.0), (128, 5e5, 8192, 8.0),
+                                                    (128, 1e4, 4096, 16.0), (16, 100.0, 1 << 20, 2.0)])
+def test_ramp_frequencies_blend_up_to_the_slow_end(rot, base, length, factor):
+    """Also where even the lowest pair turns more than beta_slow times: the ramp's end lies past the last pair then,
+    and that pair is blended like the others."""
+    freq, _ = W.rope_frequencies(rot, base, scaling="ramp", factor=factor, original_length=length)
+    plain, _ = W.rope_frequencies(rot, base)
+    pairs = rot // 2
+    # pair p turns length / (2 pi) * base^(-p / pairs) times
+    place = lambda turns: pairs * math.log(length / (2 * math.pi * turns), base)
+    lo, hi = max(math.floor(place(32.0)), 0), min(math.ceil(place(1.0)), rot - 1)
+    for j in range(pairs):
+        share = min(max((j - lo) / (hi - lo), 0.0), 1.0)
+        want = float(plain[j]) * (1.0 - share + share / factor)
+        assert abs(float(freq[j]) / want - 1) < 1e-6, j
+        if length * float(plain[j]) / (2 * math.pi) > 1.0:  # turns more than beta_slow times
+            assert float(freq[j]) > 1.000001 * float(plain[j]) / factor, j
+
+
+def test_ramp_of_a_long_original_length():
+    freq, _ = W.rope_frequencies(128, scaling="ramp", factor=8.0, original_length=131072)
+    plain, _ = W.rope_frequencies(128)
+    assert abs(float(freq[-1] / plain[-1]) - 0.370) < 5e-4

@@ -143,8 +143,8 @@ def rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_
     scaling: "none"; "linear" (positions divided by factor); "base" (the base raised so that the
     lowest frequency is divided by factor and the highest is kept); "ramp" (frequencies that turn at
     least beta_fast times in original_length are kept, those that turn at most beta_slow times
-    are divided by factor, between them a linear blend over the pair's index; attention_factor =
-    0.1 ln(factor) + 1)."""
+    are divided by factor, between them a linear blend over the pair's index, whose end may lie past the
+    last pair, at index rot - 1 at most; attention_factor = 0.1 ln(factor) + 1)."""
     torch = _torch()
     if rot < 2 or rot % 2 or not base > 1.0 or not factor >= 1.0:
         raise ValueError("rot must be a positive even number, base above 1 and factor at least 1")
@@ -160,7 +160,7 @@ def rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_
             raise ValueError("ramp scaling needs original_length and beta_fast > beta_slow > 0")
         # the (real) pair index whose frequency turns `turns` times in the original length
         at = lambda turns: pairs * math.log(original_length / (2 * math.pi * turns)) / math.log(base)
-        lo, hi = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), pairs - 1)
+        lo, hi = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), rot - 1)
         slow = ((j - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         freq = freq * (1 - slow) + freq / factor * slow
         attention = 0.1 * math.log(factor) + 1.0
