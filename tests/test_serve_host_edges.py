@@ -29,3 +29,20 @@ def test_ramp_of_a_long_original_length():
     freq, _ = W.rope_frequencies(128, scaling="ramp", factor=8.0, original_length=131072)
     plain, _ = W.rope_frequencies(128)
     assert abs(float(freq[-1] / plain[-1]) - 0.370) < 5e-4
+
+
+def test_tensors_and_workspaces_off_the_device_are_refused():
+    """Their addresses would mean nothing to the kernels."""
+    torch = pytest.importorskip("torch")
+    gpu = torch.device("cuda:0")
+    for given in (torch.empty(1 << 16, dtype=torch.uint8), torch.empty(1 << 16, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace is on"):
+            W.serve._workspace(1 << 10, given, gpu)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on a GPU"):
+        W.LoraMatmul(z(4, 64), z(2, 8, 64), z(2, 16, 8), i(4))
+    with pytest.raises(ValueError, match="on a GPU"):
+        W.Rope(z(4, 2, 64), None, None, i(4), torch.ones(32))
+    with pytest.raises(ValueError, match="on a GPU"):
+        W.TreeAttention(z(4, 2, 64), z(16, 2, 64), z(16, 2, 64), i(1, 1), i(1), i(2), page_size=16)

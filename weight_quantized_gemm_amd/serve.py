@@ -21,7 +21,9 @@ WQ_ROPE_HALF, WQ_ROPE_INTERLEAVED = 0, 1
 
 
 def _same_device(named, device):
-    """Every tensor lives on `device` (the kernels read their pointers there)."""
+    """Every tensor lives on `device`, a GPU (the kernels read their pointers there)."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, not on {device}")
     for name, t in named.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -41,6 +43,8 @@ def _workspace(size, given, device):
     torch = _torch()
     if given is None:
         return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    if given.device != device:
+        raise ValueError(f"the workspace is on {given.device}, not on {device}")
     if given.numel() * given.element_size() < size or not given.is_contiguous():
         raise ValueError(f"the workspace needs {size} contiguous bytes")
     return given
