@@ -25,3 +25,30 @@ def test_tree_long_sequences_among_short_ones(hq, hkv, d, dt):
     for _ in range(5):
         out = torch.full_like(c["q"], 9.0)
         close(tree_run(c, out=out), ref, bound, (hq, hkv, d))
+
+
+@pytest.mark.parametrize("which", range(3), ids=["adapters", "rope", "tree"])
+def test_calls_dropped_while_in_flight_on_another_stream(which):
+    """Memory that a call owns is not handed out again before the call has ended there."""
+    say("serve dropped", which)
+    call = base.make_calls()[0][which]
+    want = base.flat(call())
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        call = base.make_calls()[0][which]
+        outs = [t for t in (call.out if isinstance(call.out, tuple) else (call.out,))]
+        own = outs[0] if which == 1 else call.workspace
+        at, shape, kind = own.data_ptr(), own.shape, own.dtype
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        call(handle)
+        held = [] if which == 1 else outs
+        del call, own, outs
+        for _ in range(32):  # of the size that was just given back, on the stream that it was allocated on
+            again = torch.zeros(shape, dtype=kind, device=DEV)
+            assert again.data_ptr() != at
+            held.append(again)
+        side.synchronize()
+        if which != 1:
+            assert torch.equal(held[0], want[0])

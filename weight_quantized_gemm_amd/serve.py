@@ -6,7 +6,10 @@ Like the rest of the binding this only marshals arguments: each operator is a pr
 class: descriptors, outputs and workspace settled once, a call only enqueues kernels) and a
 one-shot function of the same arguments.  A prepared call reads its tensors anew each time, so
 a serving loop writes the next step's tokens, indices and lengths into the same tensors; it
-holds references to them, and their storage must not change.
+holds references to them, and their storage must not change.  Calls of one prepared call share its
+output and workspace: on several streams they are ordered by the caller, like all uses of a
+tensor.  It may be dropped while its calls are in flight, but not before the last replay of a graph
+that captured one.
 """
 from __future__ import annotations
 
@@ -35,8 +38,40 @@ def _handle(stream, device):
     if stream is None:
         raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return ctypes.c_void_p(raw(device.index))
-    return _stream_handle(stream, device)
+            return raw(device.index)
+    return _stream_handle(stream, device).value or 0
+
+
+class _Prepared:
+    """What prepared calls share.  A subclass sets `out`, the call's tensors and the C function with its
+    arguments up to the stream."""
+
+    def _settle(self, device, out, tensors, fn, args):
+        self.out, self.device = out, device
+        self._keep = [t for t in tensors if t is not None]
+        self._fn, self._args = fn, args
+        self._streams = {_handle(None, device)}
+
+    def __call__(self, stream=None):
+        handle = _handle(stream, self.device)
+        if handle not in self._streams:
+            self._used_on(handle)
+        status = self._fn(*self._args, handle)
+        if status:
+            _check(status)
+        return self.out
+
+    def _used_on(self, handle):
+        """The allocator is told, once, that a further stream uses the tensors: memory freed while a call is in
+        flight there is not handed out before it ends.  A captured call is none that can be waited for."""
+        torch = _torch()
+        stream = torch.cuda.ExternalStream(handle, device=self.device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        for t in self._keep:
+            t.record_stream(stream)
+        self._streams.add(handle)
 
 
 def _workspace(size, given, device):
@@ -50,7 +85,7 @@ def _workspace(size, given, device):
     return given
 
 
-class LoraMatmul:
+class LoraMatmul(_Prepared):
     """Prepared call of :func:`lora_matmul` (the same arguments); ``call(stream=None)`` enqueues
     the kernels on `stream` (default: torch's current stream) and returns ``out``."""
 
@@ -67,17 +102,9 @@ class LoraMatmul:
         _check(L.wq_lora_matmul_get_workspace_size(*map(_ref, self._descs), ctypes.byref(ws)))
         self.workspace_size = int(ws.value)
         self.workspace = _workspace(self.workspace_size, workspace, device)
-        self.out, self.device = out, device
-        self._keep = tensors
-        self._fn = L.wq_lora_matmul
-        self._args = (*map(_ref, self._descs), ctypes.c_void_p(self.workspace.data_ptr()),
-                      ctypes.c_uint64(self.workspace.numel() * self.workspace.element_size()))
-
-    def __call__(self, stream=None):
-        status = self._fn(*self._args, _handle(stream, self.device))
-        if status:
-            _check(status)
-        return self.out
+        self._settle(device, out, [*tensors.values(), self.workspace], L.wq_lora_matmul,
+                     (*map(_ref, self._descs), ctypes.c_void_p(self.workspace.data_ptr()),
+                      ctypes.c_uint64(self.workspace.numel() * self.workspace.element_size())))
 
 
 def lora_matmul(x1, a, b, indices, scale=None, *, ranks=None, x3=None, out=None, workspace=None, stream=None):
@@ -92,7 +119,7 @@ def lora_matmul(x1, a, b, indices, scale=None, *, ranks=None, x3=None, out=None,
         return LoraMatmul(x1, a, b, indices, scale, ranks=ranks, x3=x3, out=out, workspace=workspace)(s)
 
 
-class Rope:
+class Rope(_Prepared):
     """Prepared call of :func:`rope` (the same arguments); ``call(stream=None)`` enqueues the kernel
     and returns ``(q_out, k_out, v_out)``."""
 
@@ -111,17 +138,9 @@ class Rope:
         _same_device({**tensors, **outs}, device)
         self._ins = [_desc(t) for t in tensors.values()]
         self._outs = [_desc(t) for t in outs.values()]
-        self.out, self.device = (q_out, k_out, v_out), device
-        self._keep = (tensors, outs)
-        self._fn = lib().wq_rope
         layout = WQ_ROPE_INTERLEAVED if interleaved else WQ_ROPE_HALF
-        self._args = (*map(_ref, self._ins), layout, float(attention_factor), *map(_ref, self._outs))
-
-    def __call__(self, stream=None):
-        status = self._fn(*self._args, _handle(stream, self.device))
-        if status:
-            _check(status)
-        return self.out
+        self._settle(device, (q_out, k_out, v_out), [*tensors.values(), *outs.values()], lib().wq_rope,
+                     (*map(_ref, self._ins), layout, float(attention_factor), *map(_ref, self._outs)))
 
 
 def rope(q, k, v, positions, inv_freq, *, slots=None, interleaved=False, attention_factor=1.0, q_out=None, k_out=None,
@@ -173,7 +192,7 @@ def rope_frequencies(rot, base=10000.0, *, scaling="none", factor=1.0, original_
     return freq.to(torch.float32).to(device or "cpu"), attention
 
 
-class TreeAttention:
+class TreeAttention(_Prepared):
     """Prepared call of :func:`tree_attention` (the same arguments); ``call(stream=None)`` enqueues
     the kernels and returns ``out``."""
 
@@ -195,18 +214,10 @@ class TreeAttention:
                                                       ctypes.byref(ws)))
         self.workspace_size = int(ws.value)
         self.workspace = _workspace(self.workspace_size, workspace, device)
-        self.out, self.device = out, device
-        self._keep = tensors
-        self._fn = L.wq_tree_attention
-        self._args = (*map(_ref, self._descs), int(page_size), scale, _ref(self._out),
+        self._settle(device, out, [*tensors.values(), out, self.workspace], L.wq_tree_attention,
+                     (*map(_ref, self._descs), int(page_size), scale, _ref(self._out),
                       ctypes.c_void_p(self.workspace.data_ptr()),
-                      ctypes.c_uint64(self.workspace.numel() * self.workspace.element_size()))
-
-    def __call__(self, stream=None):
-        status = self._fn(*self._args, _handle(stream, self.device))
-        if status:
-            _check(status)
-        return self.out
+                      ctypes.c_uint64(self.workspace.numel() * self.workspace.element_size())))
 
 
 def tree_attention(q, k_cache, v_cache, block_table, context_lens, q_starts, tree_mask=None, *, page_size, scale=None,
