@@ -52,3 +52,32 @@ def test_calls_dropped_while_in_flight_on_another_stream(which):
         side.synchronize()
         if which != 1:
             assert torch.equal(held[0], want[0])
+
+
+@pytest.mark.parametrize("rows", [1, 8, 32, 48, 112, 200])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+def test_tree_small_weights_count(dt, d, rows):
+    """Every 32nd key has the largest score and a value of 0; the result is what the others, 2^-17 to 2^-25 of it, add.
+    Scores are exact here.  A weight is off by 2^-8 (bf16) or 2^-11 (fp16) of it, or 2^-32 of the largest
+    (fp16), and by the 2^-21 of its base-2 exponent's rounding."""
+    say("tree small weights", dt, d, rows)
+    keys = 1024
+    g = gen(97)
+    c = tree_case(97, dt, [(keys - 1, 1)], rows, 1, d, 16, None)
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1.0
+    order = torch.arange(keys)
+    slot = (c["table"].cpu()[0, order // 16].long() * 16 + order % 16).to(DEV)
+    score = -(96 + torch.randint(0, 44, (keys,), generator=g)).float() / 8  # -12 to -17.4
+    score[::32] = 0.0
+    c["k"].zero_()
+    c["k"][slot, 0, 0] = score.to(dt).to(DEV)
+    v = 1000 + 1000 * torch.rand(keys, d, generator=g)
+    v[::32] = 0.0
+    c["v"][slot, 0] = v.to(dt).to(DEV)
+    p = score.double().softmax(0)
+    vd = c["v"][slot, 0].double().cpu()
+    ref = (p @ vd).expand(1, rows, d)
+    low = 2.0 ** -32 * float(p.max()) * vd.sum(0) if dt == torch.float16 else 0.0
+    close(tree_run(c, scale=1.0), ref, 2 * base.U[dt] * ref + base.SUB[dt] + low + 2.0 ** -20 * ref, rows)

@@ -28,14 +28,15 @@
 // keys each.  The weights never leave the registers.
 //
 // Scores, sums and outputs are fp32 (base 2: scale * log2(e) is folded into the scores).  The base
-// that is taken off a row's scores is the maximum of the tile that last set it.  Weights may reach
-// 2^kSlack, which fp32 and both 16-bit types hold; a tile whose weights pass that is taken again,
+// that is taken off a row's scores is the maximum of the tile that last set it, less kLow.  Weights may reach
+// 2^(kLow + kSlack), which fp32 and both 16-bit types hold; a tile whose weights pass that is taken again,
 // with its maximum found, the base raised and the outputs rescaled.  Most tiles thus find no
 // maximum at all, which costs as many vector instructions as the weights themselves.  The
 // weights are rounded to 16 bits for the second product.  The keys kernel, whose matrix cores wait for
-// memory anyway, takes what the rounding left as a second 16-bit term, and is as exact as fp32
-// weights; the rows kernel does not, for an error of at most 2^-8 (bf16) or 2^-11 (fp16) of each
-// weight, of the size of the result's own rounding.  The sums are taken of the rounded weights,
+// memory anyway, takes what the rounding left as a second 16-bit term, for an error of at most 2^-16 (bf16) or 2^-22 (fp16)
+// of each weight; the rows kernel does not, for an error of at most 2^-8 (bf16) or 2^-11 (fp16) of each
+// weight, of the size of the result's own rounding.  In fp16 either may also lose 2^-32 of the largest
+// weight, less than the sums' own rounding.  The sums are taken of the rounded weights,
 // by the matrix cores (against ones), so that the weights add up to 1 exactly.
 //
 // Measured (MI355X, both kernels of a call):
@@ -88,7 +89,11 @@ struct TreeArgs {
   uint32_t q_and, q_xor;
 };
 
-constexpr int kSlack = 8;       // log2 of the largest weight
+// A base stands kLow below the maximum that sets it, and a weight may pass that maximum's by 2^kSlack.  bf16 has the
+// range of fp32; of fp16's, all of the upper end is used: a weight's last place is 2^-24, so that one loses at
+// most 2^-32 of the largest there (2^-25 with a base at the maximum, which summed up over a long context).
+constexpr int kSlack = 8;
+template <bool BF16> constexpr int kLow = BF16 ? 0 : 7;
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 constexpr float kNone = -__builtin_inff();
 
@@ -373,7 +378,7 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
       for (int h = 0; h < KB; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][h][i]);
-      const float now = fmaxf(w.m[t0 + t], across_max(top) * a.scale);
+      const float now = fmaxf(w.m[t0 + t], across_max(top) * a.scale - kLow<BF16>);
       const float keep = __builtin_amdgcn_exp2f(w.m[t0 + t] - (now == kNone ? 0.f : now));
       w.m[t0 + t] = now;
       w.l[t0 + t] *= keep;
@@ -412,7 +417,7 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
     }
   }
   if constexpr (!SLOW) {
-    constexpr uint16_t kMost = BF16 ? (127 + kSlack) << 7 : (15 + kSlack) << 10;
+    constexpr uint16_t kMost = BF16 ? (127 + kSlack) << 7 : (15 + kLow<BF16> + kSlack) << 10;
     if (__ballot(most[0] > kMost || most[1] > kMost)) {
       __builtin_amdgcn_s_setprio(0);
       return false;
