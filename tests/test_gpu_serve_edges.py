@@ -81,3 +81,35 @@ def test_tree_small_weights_count(dt, d, rows):
     ref = (p @ vd).expand(1, rows, d)
     low = 2.0 ** -32 * float(p.max()) * vd.sum(0) if dt == torch.float16 else 0.0
     close(tree_run(c, scale=1.0), ref, 2 * base.U[dt] * ref + base.SUB[dt] + low + 2.0 ** -20 * ref, rows)
+
+
+# hq, hkv, d, tokens: every tile height, number of waves and head size that a call may get
+VARIANTS = [(4, 2, 64, 3), (8, 2, 64, 7), (8, 2, 64, 11), (8, 1, 64, 13), (16, 1, 64, 12), (4, 2, 128, 3), (8, 2, 128, 7),
+            (8, 2, 128, 11), (8, 1, 128, 13), (16, 1, 128, 12), (4, 2, 256, 3), (16, 1, 256, 4)]
+VIDS = ["h%d_%d_d%d_t%d" % v for v in VARIANTS]
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("variant", VARIANTS, ids=VIDS)
+def test_tree_infinities_of_the_context(variant, dt):
+    """Infinities in V give infinities of their sign, both signs or a NaN give NaN, wherever the key stands and
+    however little its weight is; other columns and other cached heads stay what they are."""
+    hq, hkv, d, tokens = variant
+    say("tree seen infinities", variant, dt)
+    c = tree_case(111, dt, [(500, tokens), (300, tokens)], hq, hkv, d, 16, "tree", std=3.0)
+    clean = tree_run(c)
+    odd = torch.zeros(hkv, d, dtype=torch.bool)
+    g = gen(112)
+    for b, ctx in enumerate((500, 300)):
+        for key in (0, 31, 32, 33, 100, 127, 128, 250, ctx - 1, ctx):
+            slot = int(c["table"][b, key // 16]) * 16 + key % 16
+            h, col = int(torch.randint(0, hkv, (), generator=g)), int(torch.randint(0, d // 2, (), generator=g))
+            c["v"][slot, h, col] = (float("inf"), -float("inf"), float("nan"))[key % 3 if key < 128 else 0]
+            odd[h, col] = True
+    out = tree_run(c)
+    ref, bound = tree_ref(c)
+    close(out, ref, bound, variant)
+    assert torch.isinf(out).any()
+    same = ~odd.repeat_interleave(hq // hkv, 0).to(DEV)
+    # (bases do not move between the two ways: the same weights, up to the rounding of their sums)
+    assert torch.isfinite(out[:, same]).all() and (out[:, same] - clean[:, same]).abs().max() < 0.1

@@ -228,7 +228,9 @@ __device__ __forceinline__ bool not_finite(uint32_t half) {
 // Edge tiles hold keys that some row does not see: past the end, on no page, or drafted tokens.
 // The scores of unseen keys become -inf there, and V loses, for the matrix product, its rows
 // without a key and its infinities and NaN (0 * inf would reach rows that do not see them); what
-// those contribute to rows that do see them is added afterwards.
+// those contribute to rows that do see them is added afterwards, with fp32 weights.  In a tile that is no
+// edge they are met by the product, whose 16-bit terms make a NaN of an infinity where they have
+// unlike signs or are 0: a piece of work whose outputs show any (finite) is taken again, with all its tiles as edges.
 
 // Bit r: whether key r of the tile exists.
 template <int KT>
@@ -507,6 +509,19 @@ __device__ __forceinline__ void compute_slow(const TreeArgs& a, const Seq& s, co
     compute_rows<HD, BF16, RT, 1, KT, true, TWO>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
 }
 
+// Whether a wave's outputs are all finite.
+template <int HD, int RT>
+__device__ __forceinline__ bool finite(const Rows<HD, RT>& w) {
+  float z = 0.f;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int d = 0; d < HD / 16; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z = fmaf(w.o[t][d][i], 0.f, z);
+  return z == 0.f;
+}
+
 // 1 / sum; no key seen: 0; NaN stays
 __device__ __forceinline__ float inverse(float sum) { return sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f; }
 
@@ -615,52 +630,54 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
     const uint16_t* kh = a.k + (int64_t)p.kvh * a.k_h;
     const uint16_t* vh = a.v + (int64_t)p.kvh * a.v_h;
     Rows<HD, RT> w;
-    start_rows<HD, BF16, RT>(a, p.s, p.kvh, p.row0, p.rows, lane, w);
-
     uint8_t* mine = lds + wave * 2 * C::Stage;
     const uint32_t to = lds_address(lds) + wave * 2 * C::Stage;
-    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += L::Slots) {
-      const int count = min(L::Slots, p.key_hi - key0);
-      __syncthreads();  // the slots (and the joining rows in the stages) have been read
-      const int lost = uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
-      const int tiles = (count + 31) / 32;
-      wave_wait<0>();  // from here on the loads in flight are the tiles'
-      if (wave < tiles) load_tile<HD, 32, 1>(a, kh, vh, slots, 32 * wave, to, 0, lane);
-      // Tiles j = wave, wave + NW, ...; stage of tile j: its turn's parity.
-      int j = wave, st = 0;
-      auto begin = [&]() {  // the next tile is on its way, this one is here; whether it is an edge tile
-        const int first = 32 * j;
-        if (j + NW < tiles) {
-          load_tile<HD, 32, 1>(a, kh, vh, slots, first + 32 * NW, to + (st ^ 1) * C::Stage, 0, lane);
-          wave_wait<2 * C::Loads>();
-        } else {
-          wave_wait<0>();
+    for (int again = 0;; again = 1) {
+      start_rows<HD, BF16, RT>(a, p.s, p.kvh, p.row0, p.rows, lane, w);
+      for (int key0 = p.key_lo; key0 < p.key_hi; key0 += L::Slots) {
+        const int count = min(L::Slots, p.key_hi - key0);
+        __syncthreads();  // the slots (and the joining rows in the stages) have been read
+        const int lost = again | uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
+        const int tiles = (count + 31) / 32;
+        wave_wait<0>();  // from here on the loads in flight are the tiles'
+        if (wave < tiles) load_tile<HD, 32, 1>(a, kh, vh, slots, 32 * wave, to, 0, lane);
+        // Tiles j = wave, wave + NW, ...; stage of tile j: its turn's parity.
+        int j = wave, st = 0;
+        auto begin = [&]() {  // the next tile is on its way, this one is here; whether it is an edge tile
+          const int first = 32 * j;
+          if (j + NW < tiles) {
+            load_tile<HD, 32, 1>(a, kh, vh, slots, first + 32 * NW, to + (st ^ 1) * C::Stage, 0, lane);
+            wave_wait<2 * C::Loads>();
+          } else {
+            wave_wait<0>();
+          }
+          return lost || first + 32 > count || key0 + first - p.s.ctx + 32 > 0;
+        };
+        auto end = [&]() {
+          // every read of this stage has returned before the next load into it
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          j += NW;
+          st ^= 1;
+        };
+        while (j < tiles) {
+          bool edge = false;
+          for (; j < tiles; end()) {
+            edge = begin();
+            if (edge || !compute_fast<HD, BF16, RT, 32, true>(a, mine + st * C::Stage, lane, w)) break;
+          }
+          if (j >= tiles) break;
+          uint8_t* stage = mine + st * C::Stage;
+          uint64_t keys = 0, odd = 0;
+          if (edge) {
+            keys = tile_keys<32>(slots, 32 * j, lane);
+            odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
+            __builtin_amdgcn_wave_barrier();
+          }
+          compute_slow<HD, BF16, RT, 32, true>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+          end();
         }
-        return lost || first + 32 > count || key0 + first - p.s.ctx + 32 > 0;
-      };
-      auto end = [&]() {
-        // every read of this stage has returned before the next load into it
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        j += NW;
-        st ^= 1;
-      };
-      while (j < tiles) {
-        bool edge = false;
-        for (; j < tiles; end()) {
-          edge = begin();
-          if (edge || !compute_fast<HD, BF16, RT, 32, true>(a, mine + st * C::Stage, lane, w)) break;
-        }
-        if (j >= tiles) break;
-        uint8_t* stage = mine + st * C::Stage;
-        uint64_t keys = 0, odd = 0;
-        if (edge) {
-          keys = tile_keys<32>(slots, 32 * j, lane);
-          odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
-          __builtin_amdgcn_wave_barrier();
-        }
-        compute_slow<HD, BF16, RT, 32, true>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
-        end();
       }
+      if (again || !__syncthreads_or(!finite(w))) break;
     }
 
     // the waves' results meet in LDS, in the place of the stages
@@ -748,43 +765,46 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
     const uint16_t* vh = a.v + (int64_t)p.kvh * a.v_h;
     const int row0 = p.row0 + 16 * RT * wave;
     Rows<HD, RT> w;
-    start_rows<HD, BF16, RT>(a, p.s, p.kvh, row0, p.rows, lane, w);
-    for (int key0 = p.key_lo; key0 < p.key_hi; key0 += RowsLds<HD, NW>::Slots) {
-      const int count = min(RowsLds<HD, NW>::Slots, p.key_hi - key0);
-      __syncthreads();  // the slots and stages have been read
-      const int lost = uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
-      const int tiles = (count + KT - 1) / KT;
-      wave_wait<0>();
-      const uint32_t to = lds_address(lds);
-      load_tile<HD, KT, NW>(a, kh, vh, slots, 0, to, wave, lane);
-      int j = 0;
-      // The workgroup's waves may leave the inner loop at different tiles: a wave in compute_slow takes
-      // part in the barriers of its next tile when it gets there.  Only edge tiles, which are edges for
-      // all, hold barriers of their own.
-      while (j < tiles) {
-        bool edge = false;
-        for (; j < tiles; ++j) {
-          // this tile has landed for every wave, and every wave has read the one before it
-          stage_barrier<0>();
-          if (j + 1 < tiles)
-            load_tile<HD, KT, NW>(a, kh, vh, slots, KT * (j + 1), to + ((j + 1) & 1) * C::Stage, wave, lane);
-          edge = lost || KT * (j + 1) > count || key0 + KT * (j + 1) - p.s.ctx > 0;
-          if (edge || !compute_fast<HD, BF16, RT, KT, false>(a, lds + (j & 1) * C::Stage, lane, w)) break;
+    for (int again = 0;; again = 1) {
+      start_rows<HD, BF16, RT>(a, p.s, p.kvh, row0, p.rows, lane, w);
+      for (int key0 = p.key_lo; key0 < p.key_hi; key0 += RowsLds<HD, NW>::Slots) {
+        const int count = min(RowsLds<HD, NW>::Slots, p.key_hi - key0);
+        __syncthreads();  // the slots and stages have been read
+        const int lost = again | uniform(__syncthreads_or(find_slots(a, p.b, key0, count, slots, tid, 64 * NW)));
+        const int tiles = (count + KT - 1) / KT;
+        wave_wait<0>();
+        const uint32_t to = lds_address(lds);
+        load_tile<HD, KT, NW>(a, kh, vh, slots, 0, to, wave, lane);
+        int j = 0;
+        // The workgroup's waves may leave the inner loop at different tiles: a wave in compute_slow takes
+        // part in the barriers of its next tile when it gets there.  Only edge tiles, which are edges for
+        // all, hold barriers of their own.
+        while (j < tiles) {
+          bool edge = false;
+          for (; j < tiles; ++j) {
+            // this tile has landed for every wave, and every wave has read the one before it
+            stage_barrier<0>();
+            if (j + 1 < tiles)
+              load_tile<HD, KT, NW>(a, kh, vh, slots, KT * (j + 1), to + ((j + 1) & 1) * C::Stage, wave, lane);
+            edge = lost || KT * (j + 1) > count || key0 + KT * (j + 1) - p.s.ctx > 0;
+            if (edge || !compute_fast<HD, BF16, RT, KT, false>(a, lds + (j & 1) * C::Stage, lane, w)) break;
+          }
+          if (j >= tiles) break;
+          uint8_t* stage = lds + (j & 1) * C::Stage;
+          uint64_t keys = 0, odd = 0;
+          if (edge) {
+            keys = tile_keys<KT>(slots, KT * j, lane);
+            const uint64_t mine = clean_values<HD, BF16, KT, NW>(stage, keys, wave, lane);
+            if (lane == 0) odd_of[wave] = mine;
+            __syncthreads();
+  #pragma unroll
+            for (int i = 0; i < NW; ++i) odd |= odd_of[i];
+          }
+          compute_slow<HD, BF16, RT, KT, false>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+          ++j;
         }
-        if (j >= tiles) break;
-        uint8_t* stage = lds + (j & 1) * C::Stage;
-        uint64_t keys = 0, odd = 0;
-        if (edge) {
-          keys = tile_keys<KT>(slots, KT * j, lane);
-          const uint64_t mine = clean_values<HD, BF16, KT, NW>(stage, keys, wave, lane);
-          if (lane == 0) odd_of[wave] = mine;
-          __syncthreads();
-#pragma unroll
-          for (int i = 0; i < NW; ++i) odd |= odd_of[i];
-        }
-        compute_slow<HD, BF16, RT, KT, false>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
-        ++j;
       }
+      if (again || !__syncthreads_or(!finite(w))) break;
     }
 
     const int64_t part = 2 * me + (p.begins ? 1 : 0);
