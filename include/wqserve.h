@@ -122,9 +122,8 @@ int wq_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq
  *   scale         finite.
  *   output        required; q's dtype; rows (N, hq, d), not overlapping an input.
  * N == 0 or B == 0 is a call with nothing to do.  Scores, the softmax and the sums are fp32;
- * the weights p go into the product with v as one number of q's dtype, or, where the average
- * sequence has at most 32 rows (tokens x query heads of a cached head) or d = 256, as the sum of two;
- * fp16 keeps them to 2^-32 of the largest.
+ * the weights p go into the product with v as the sum of two numbers of q's dtype (in fp16 to 2^-32 of
+ * the largest), and the result is rounded once.
  */
 int wq_tree_attention_get_workspace_size(const wq_tensor* q, const wq_tensor* k_cache,
                                          const wq_tensor* v_cache, const wq_tensor* block_table,

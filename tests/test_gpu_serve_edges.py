@@ -113,3 +113,18 @@ def test_tree_infinities_of_the_context(variant, dt):
     same = ~odd.repeat_interleave(hq // hkv, 0).to(DEV)
     # (bases do not move between the two ways: the same weights, up to the rounding of their sums)
     assert torch.isfinite(out[:, same]).all() and (out[:, same] - clean[:, same]).abs().max() < 0.1
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("variant", VARIANTS, ids=VIDS)
+def test_tree_is_off_by_its_last_rounding(variant, dt):
+    """In the root mean square the result is off by what rounding the exact one once gives.  The rest are weights of
+    two 16-bit terms, 2^-16 (bf16) or 2^-22 (fp16) of each, and scores of about 10 whose fp32 sums are off by a
+    few 2^-24 of that, 2^-18 of a weight: a hundredth of the rounding to 2^-8 or 2^-11, which adds in the
+    squares.  One 16-bit term would add another rounding of the result's own size, a factor of 1.4."""
+    hq, hkv, d, tokens = variant
+    say("tree rms", variant, dt)
+    c = tree_case(121, dt, [(700, tokens), (400, tokens)], hq, hkv, d, 16, "tree")
+    ref, _ = tree_ref(c)
+    rms = lambda x: float(x.square().mean().sqrt())
+    assert rms(tree_run(c).double().cpu() - ref) < 1.05 * rms(ref.to(dt).double() - ref)

@@ -66,13 +66,13 @@ TreePlan plan_tree(const TreeProblem& p) {
   if (p.N == 0 || p.B == 0) return pl;
   // Rows (tokens x heads that share a cached head) of the average sequence: a tile of too many rows
   // only pads, one of too few reads the keys again.  bf16, d = 128, 8 cached heads, 8192 keys:
-  //   16 rows, 32 sequences: tiles of 16 rows 195 us, of 32 200 us
-  //   20 rows, 32 sequences: tiles of 16 rows 374 us, of 32 201 us
-  //   32 rows, 32 sequences: waves that split the keys 205 us, that split the rows (64) 210 us
-  //   48 rows, 16 sequences: waves that split the keys 134 us, that split the rows (64) 124 us
-  //   64 rows, 16 sequences: 2 waves 127 us, 4 125 us;  48 rows of 4 cached heads: 70 us, 74 us
-  //   112 rows, 16 sequences: 2 waves 138 us, 4 130 us, 8 180 us
-  //   256 rows, 16 sequences: 4 waves 195 us, 8 186 us;  512 rows, 8 sequences: 182 us, 172 us
+  //   16 rows, 32 sequences: tiles of 16 rows 203 us, of 32 208 us
+  //   20 rows, 32 sequences: tiles of 16 rows 383 us, of 32 204 us
+  //   32 rows, 32 sequences: waves that split the keys 209 us, that split the rows (64) 221 us
+  //   48 rows, 16 sequences: waves that split the keys 132 us, that split the rows (64) 126 us
+  //   64 rows, 16 sequences: 2 waves 128 us, 4 141 us;  48 rows of 4 cached heads: 74 us, 79 us
+  //   112 rows, 16 sequences: 2 waves 155 us, 4 143 us, 8 221 us
+  //   256 rows, 16 sequences: 4 waves 240 us, 8 228 us;  512 rows, 8 sequences: 229 us, 218 us
   // At d = 256 the outputs of a wave of more than 16 rows, or any of the other kernel, would not
   // fit its registers.
   const int64_t rows = ceil_div(p.N, std::min(p.N, p.B)) * p.group;

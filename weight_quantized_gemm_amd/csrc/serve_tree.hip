@@ -31,13 +31,12 @@
 // that is taken off a row's scores is the maximum of the tile that last set it, less kLow.  Weights may reach
 // 2^(kLow + kSlack), which fp32 and both 16-bit types hold; a tile whose weights pass that is taken again,
 // with its maximum found, the base raised and the outputs rescaled.  Most tiles thus find no
-// maximum at all, which costs as many vector instructions as the weights themselves.  The
-// weights are rounded to 16 bits for the second product.  The keys kernel, whose matrix cores wait for
-// memory anyway, takes what the rounding left as a second 16-bit term, for an error of at most 2^-16 (bf16) or 2^-22 (fp16)
-// of each weight; the rows kernel does not, for an error of at most 2^-8 (bf16) or 2^-11 (fp16) of each
-// weight, of the size of the result's own rounding.  In fp16 either may also lose 2^-32 of the largest
-// weight, less than the sums' own rounding.  The sums are taken of the rounded weights,
-// by the matrix cores (against ones), so that the weights add up to 1 exactly.
+// maximum at all, which costs as many vector instructions as the weights themselves.  A weight
+// enters the second product as two 16-bit terms, itself rounded and what the rounding left, for an error of at most
+// 2^-16 (bf16) or 2^-22 (fp16) of it, and in fp16 2^-32 of the largest, less than the sums' own
+// rounding.  One term would be off by as much as the result's last rounding is; the second costs nothing where
+// memory bounds the kernel, and up to 28 % where the matrix cores do (512 rows: 240 -> 305 us).  The sums
+// are taken of the same two terms, by the matrix cores (against ones), so that the weights add up to 1 exactly.
 //
 // Measured (MI355X, both kernels of a call):
 //   64 single tokens over 16 to 8192 keys, 8 cached heads of 128, fp16: 248 us for 1.36 GB, 5.5 TB/s; reads
@@ -327,8 +326,8 @@ __device__ __forceinline__ void start_rows(const TreeArgs& a, const Seq& s, int 
 // tile it takes `keys` that exist, drafted tokens from draft0 on (the tile's first key; at most -KT: none),
 // and the rows `odd` of V that clean_values took infinities or NaN from.  Otherwise all keys are seen and
 // the bases stay; returns false, with nothing summed, where a row has no base yet or a weight
-// passes 2^kSlack.
-template <int HD, bool BF16, int RT, int NT, int KT, bool SLOW, bool TWO>
+// passes 2^(kLow + kSlack).
+template <int HD, bool BF16, int RT, int NT, int KT, bool SLOW>
 __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, const int* slots, int first, int draft0,
                                              uint64_t keys, uint64_t odd, const uint8_t* stage, const uint16_t* vh,
                                              int lane, const int t0, Rows<HD, RT>& w) {
@@ -389,7 +388,7 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
     }
   }
 
-  u32x4_t pf[NT][KT / 32], pl[NT][KT / 32];  // TWO: pl, what the rounding of pf left
+  u32x4_t pf[NT][KT / 32], pl[NT][KT / 32];  // pl: what the rounding of pf left
   u16x2_t most = {0, 0};  // of the weights' bits, which order like the weights (a NaN is above all)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -403,13 +402,6 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
       pf[t][b] = u32x4_t{pack2<BF16>(sc[t][2 * b][0], sc[t][2 * b][1]), pack2<BF16>(sc[t][2 * b][2], sc[t][2 * b][3]),
                          pack2<BF16>(sc[t][2 * b + 1][0], sc[t][2 * b + 1][1]),
                          pack2<BF16>(sc[t][2 * b + 1][2], sc[t][2 * b + 1][3])};
-      if constexpr (TWO)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p0 = sc[t][2 * b + e / 2][2 * (e & 1)], p1 = sc[t][2 * b + e / 2][2 * (e & 1) + 1];
-          pl[t][b][e] = pack2<BF16>(p0 - act_to_f32<BF16>((uint16_t)pf[t][b][e]),
-                                    p1 - act_to_f32<BF16>((uint16_t)(pf[t][b][e] >> 16)));
-        }
       asm volatile("" : "+v"(pf[t][b]));  // rounded once: it is not made again for the product
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -428,21 +420,24 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
 
   if constexpr (!SLOW) __builtin_amdgcn_s_setprio(0);
   constexpr uint32_t kOne2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int b = 0; b < KT / 32; ++b)
-    {
-      w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pf[t][b], w.l[t0 + t]);
-      if constexpr (TWO) w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pl[t][b], w.l[t0 + t]);
-    }
 
   // V^T: column 16 d + l16, keys 4 g .. + 3 and 16 + 4 g .. + 3 of each 32; rows 16 apart and columns 16
   // apart as above
   const uint32_t vr = 4 * g + (l16 >> 2), v0 = vr * C::RB + 16 * v_chunk<HD>(vr, (l16 & 3) >> 1) + 8 * (l16 & 1);
   const uint8_t* vs = stage + C::Half;
 #pragma unroll
-  for (int b = 0; b < KT / 32; ++b)
+  for (int b = 0; b < KT / 32; ++b) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pf[t][b], w.l[t0 + t]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p0 = sc[t][2 * b + e / 2][2 * (e & 1)], p1 = sc[t][2 * b + e / 2][2 * (e & 1) + 1];
+        pl[t][b][e] = pack2<BF16>(p0 - act_to_f32<BF16>((uint16_t)pf[t][b][e]),
+                                  p1 - act_to_f32<BF16>((uint16_t)(pf[t][b][e] >> 16)));
+      }
+      w.l[t0 + t] = mfma16x16x32<BF16>(u32x4_t{kOne2, kOne2, kOne2, kOne2}, pl[t][b], w.l[t0 + t]);
+    }
 #pragma unroll
     for (int d = 0; d < HD / 16; ++d) {
       const u32x2_t lo = lds_read_tr16(vs + (v0 ^ (32 * d)) + 32 * b * C::RB);
@@ -451,9 +446,10 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pf[t][b], w.o[t0 + t][d]);
-        if constexpr (TWO) w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pl[t][b], w.o[t0 + t][d]);
+        w.o[t0 + t][d] = mfma16x16x32<BF16>(vf, pl[t][b], w.o[t0 + t][d]);
       }
     }
+  }
 
   if constexpr (SLOW) {
     while (odd) {
@@ -488,14 +484,14 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
 }
 
 // All of a wave's row blocks: at once, where that will do (false: nothing was done) ...
-template <int HD, bool BF16, int RT, int KT, bool TWO>
+template <int HD, bool BF16, int RT, int KT>
 __device__ __forceinline__ bool compute_fast(const TreeArgs& a, const uint8_t* stage, int lane, Rows<HD, RT>& w) {
-  return compute_rows<HD, BF16, RT, RT, KT, false, TWO>(a, Seq{}, nullptr, 0, 0, 0, 0, stage, nullptr, lane, 0, w);
+  return compute_rows<HD, BF16, RT, RT, KT, false>(a, Seq{}, nullptr, 0, 0, 0, 0, stage, nullptr, lane, 0, w);
 }
 // ... or one by one, which takes fewer registers.  The loops over tiles below keep to the first form
 // and leave for the second: in one loop with both, the outputs would change registers at every
 // tile (40 moves).
-template <int HD, bool BF16, int RT, int KT, bool TWO>
+template <int HD, bool BF16, int RT, int KT>
 __device__ __forceinline__ void compute_slow(const TreeArgs& a, const Seq& s, const int* slots, int first, bool edge,
                                              int draft0, uint64_t keys, uint64_t odd, const uint8_t* stage,
                                              const uint16_t* vh, int lane, Rows<HD, RT>& w) {
@@ -506,7 +502,7 @@ __device__ __forceinline__ void compute_slow(const TreeArgs& a, const Seq& s, co
   }
 #pragma unroll
   for (int t = 0; t < RT; ++t)
-    compute_rows<HD, BF16, RT, 1, KT, true, TWO>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
+    compute_rows<HD, BF16, RT, 1, KT, true>(a, s, slots, first, draft0, keys, odd, stage, vh, lane, t, w);
 }
 
 // Whether a wave's outputs are all finite.
@@ -663,7 +659,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
           bool edge = false;
           for (; j < tiles; end()) {
             edge = begin();
-            if (edge || !compute_fast<HD, BF16, RT, 32, true>(a, mine + st * C::Stage, lane, w)) break;
+            if (edge || !compute_fast<HD, BF16, RT, 32>(a, mine + st * C::Stage, lane, w)) break;
           }
           if (j >= tiles) break;
           uint8_t* stage = mine + st * C::Stage;
@@ -673,7 +669,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
             odd = clean_values<HD, BF16, 32, 1>(stage, keys, 0, lane);
             __builtin_amdgcn_wave_barrier();
           }
-          compute_slow<HD, BF16, RT, 32, true>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+          compute_slow<HD, BF16, RT, 32>(a, p.s, slots, 32 * j, edge, key0 + 32 * j - p.s.ctx, keys, odd, stage, vh, lane, w);
           end();
         }
       }
@@ -787,7 +783,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
             if (j + 1 < tiles)
               load_tile<HD, KT, NW>(a, kh, vh, slots, KT * (j + 1), to + ((j + 1) & 1) * C::Stage, wave, lane);
             edge = lost || KT * (j + 1) > count || key0 + KT * (j + 1) - p.s.ctx > 0;
-            if (edge || !compute_fast<HD, BF16, RT, KT, false>(a, lds + (j & 1) * C::Stage, lane, w)) break;
+            if (edge || !compute_fast<HD, BF16, RT, KT>(a, lds + (j & 1) * C::Stage, lane, w)) break;
           }
           if (j >= tiles) break;
           uint8_t* stage = lds + (j & 1) * C::Stage;
@@ -797,10 +793,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const TreeArgs a)
             const uint64_t mine = clean_values<HD, BF16, KT, NW>(stage, keys, wave, lane);
             if (lane == 0) odd_of[wave] = mine;
             __syncthreads();
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < NW; ++i) odd |= odd_of[i];
           }
-          compute_slow<HD, BF16, RT, KT, false>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
+          compute_slow<HD, BF16, RT, KT>(a, p.s, slots, KT * j, edge, key0 + KT * j - p.s.ctx, keys, odd, stage, vh, lane, w);
           ++j;
         }
       }
