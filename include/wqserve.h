@@ -48,8 +48,9 @@ extern "C" {
  *   x3       optional; x1's dtype; rows, the output's shape (the shared projection's result).
  *            Absent means 0.  It may be the output itself (same address and strides).
  *   output   required; x1's dtype; rows (m, n) or (b, s, n) following x1.
- * m == 0 is a call with nothing to do.  Both products are summed in fp32; the result is
- * rounded once.  A token's result takes nothing from the other tokens' values,
+ * m == 0 is a call with nothing to do.  Both products are summed in fp32; the first enters the
+ * second to 2^-16 (bf16) or 2^-22 (fp16) of each number, in fp16 2^-39 of a token's largest; the
+ * result is rounded once.  A token's result takes nothing from the other tokens' values,
  * and equal calls give equal bits.
  */
 int wq_lora_matmul_get_workspace_size(const wq_tensor* x1, const wq_tensor* a, const wq_tensor* b,

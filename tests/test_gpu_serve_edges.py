@@ -1,5 +1,7 @@
 """The serving operators where variants, tiles and types meet their ends (GPU); references and bounds are those
 of test_gpu_serve.py."""
+import math
+
 import pytest
 import torch
 
@@ -128,3 +130,27 @@ def test_tree_is_off_by_its_last_rounding(variant, dt):
     ref, _ = tree_ref(c)
     rms = lambda x: float(x.square().mean().sqrt())
     assert rms(tree_run(c).double().cpu() - ref) < 1.05 * rms(ref.to(dt).double() - ref)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("m", [3, 70, 2100])
+@pytest.mark.parametrize("r", [16, 32, 72])
+def test_lora_numbers_far_below_the_largest(r, m, dt):
+    """One rank's first product is 2^16 to 2^22 times the others, and most columns of b are 0 there.  First products
+    are exact here; they are off by 2^-16 of each in bf16, and in fp16 by 2^-39 of the largest, 2^-17 of any."""
+    say("lora far below", r, m, dt)
+    g = gen(131)
+    k, n = 64, 136
+    x1 = torch.zeros(m, k)
+    x1[:, 0] = 2.0 ** torch.randint(-1, 2, (m,), generator=g)
+    a = torch.zeros(2, r, k)
+    a[:, :, 0] = 2.0 ** torch.empty(2, r).uniform_(-10, -4, generator=g)
+    a[0, 5, 0], a[1, 1, 0] = 4096.0, 2048.0
+    b = torch.randn(2, n, r, generator=g)
+    b[0, 8:, 5], b[1, 8:, 1] = 0.0, 0.0
+    c = dict(x1=x1.to(dt).to(DEV), a=a.to(dt).to(DEV), b=b.to(dt).to(DEV), x3=None, ranks=None,
+             indices=torch.randint(0, 2, (m,), generator=g).int().to(DEV), scale=torch.tensor([64.0, -32.0], device=DEV))
+    ref, bound = base.lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], None, None)
+    if dt == torch.float16:  # the few columns that meet the large rank may pass the type's range
+        ref = torch.where(ref.abs() >= 65520, ref.sign() * math.inf, ref)
+    close(base.lora_run(c), ref, bound, (r, m))

@@ -333,9 +333,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const Lo
 
 // ------------------------------------------------------------------------- out = x3 + h B^T
 // Both factors of this product are 16-bit in the matrix cores, but h is fp32: it is taken as
-// the sum of two 16-bit numbers, hi + lo, which keep 16 (bf16) or 22 (fp16) of its bits.  A
-// row is first scaled by a power of two to a largest magnitude in [1, 2), so that fp16 can
-// hold it; the power comes back in fp32 at the end.  The contraction of one 16x16x32 MFMA
+// the sum of two 16-bit numbers, hi + lo, which are off by at most 2^-16 (bf16) or 2^-22 (fp16) of it.  A
+// row is first scaled by a power of two to a largest magnitude in [1, 2) in bf16 and [2^14, 2^15) in fp16, whose
+// last place of 2^-24 then is 2^-38 of that (an error of 2^-39 where it is more than 2^-22 of the number); the
+// power comes back in fp32 at the end.  The contraction of one 16x16x32 MFMA
 // covers 16 ranks twice, against hi (lanes 0..31) and lo (lanes 32..63).  This product is
 // bound by x3 and out, so the doubled matrix work is free.
 //
@@ -456,7 +457,7 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
       for (int o = 1; o < TPR; o <<= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
       // 2^-e: exponent of the largest magnitude, kept where 2^-e and 2^e are normal numbers
       int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 : 0;
-      e = min(max(e, -126), 126);
+      e = min(max(e - (BF16 ? 0 : 14), -126), 126);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       if (first == 0) factor[row] = __uint_as_float((uint32_t)(127 + e) << 23);
       for (int c = first; c < 16 * nk; c += 4 * TPR) {
