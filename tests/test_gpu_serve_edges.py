@@ -154,3 +154,33 @@ def test_lora_numbers_far_below_the_largest(r, m, dt):
     if dt == torch.float16:  # the few columns that meet the large rank may pass the type's range
         ref = torch.where(ref.abs() >= 65520, ref.sign() * math.inf, ref)
     close(base.lora_run(c), ref, bound, (r, m))
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("m,r,n", [(1, 8, 8), (40, 16, 136), (300, 32, 264), (70, 136, 72), (2100, 16, 136), (2300, 200, 72)])
+def test_lora_infinities_of_b(m, r, n, dt):
+    """An infinity of b gives infinities in its column for the tokens of its adapter, of the sign that the first product
+    has, both signs a NaN; every other element is what it was."""
+    say("lora infinite b", m, r, n, dt)
+    c = base.lora_case(141, dt, m, 3, r, 520, n, order="mixed" if m > 1 else "one", ranks=m > 1)
+    clean = base.lora_run(c)
+    c["b"][0, 3, 1], c["b"][1, n - 1, r // 2], c["b"][2, 5, 0] = math.inf, -math.inf, math.inf
+    c["b"][2, 0, 0], c["b"][2, 0, 2] = math.inf, -math.inf
+    ref, bound = base.lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], c["ranks"], c["x3"])
+    out = base.lora_run(c)
+    close(out, ref, bound, (m, r, n))
+    fin = torch.isfinite(ref).to(DEV)
+    assert torch.equal(out[fin], clean[fin]) and not fin.all()
+
+
+def test_lora_sums_that_a_factor_brings_back():
+    """bf16 reaches 2^127: a tiny first product against huge numbers of b passes fp32 between the row's factor and
+    its return, not in the result."""
+    say("lora factor")
+    for m in (20, 2100):
+        c = base.lora_case(142, torch.bfloat16, m, 2, 24, 64, 72, order="mixed")
+        c["x1"] *= 2.0 ** -60
+        c["a"] *= 2.0 ** -40
+        c["b"] = (c["b"].sign() * 2.0 ** 127 * 1.5).to(torch.bfloat16)
+        ref, bound = base.lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], None, c["x3"])
+        close(base.lora_run(c), ref, bound, m)
