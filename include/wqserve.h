@@ -120,7 +120,7 @@ int wq_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq
  *                 whether it sees token j of its sequence; tokens past 32 * words are not seen.
  *                 Absent: each token sees the tokens of its sequence up to itself.
  *   page_size     in [1, 2^20].
- *   scale         finite.
+ *   scale         in [-2^127, 2^127].
  *   output        required; q's dtype; rows (N, hq, d), not overlapping an input.
  * N == 0 or B == 0 is a call with nothing to do.  Scores, the softmax and the sums are fp32;
  * the weights p go into the product with v as the sum of two numbers of q's dtype (in fp16 to 2^-32 of

@@ -46,3 +46,15 @@ def test_tensors_and_workspaces_off_the_device_are_refused():
         W.Rope(z(4, 2, 64), None, None, i(4), torch.ones(32))
     with pytest.raises(ValueError, match="on a GPU"):
         W.TreeAttention(z(4, 2, 64), z(16, 2, 64), z(16, 2, 64), i(1, 1), i(1), i(2), page_size=16)
+
+
+def test_tree_scale_whose_base_2_form_overflows_is_refused(wqlib):
+    """The kernels take scale * log2(e): beyond 2^127 that may be infinite, and a score of 0 would become NaN."""
+    import test_serve_host as host
+    a = host.tree_args()
+    t = [host.ref(x) for x in list(a.values())[:7]]
+    call = lambda scale: wqlib.wq_tree_attention(*t, 16, scale, host.ref(a["output"]), None, 1 << 40, None)
+    for scale in (2.4e38, -3.4e38, 2.0 ** 127 * (1 + 2.0 ** -20)):
+        assert call(scale) == W.WQ_ERR_PARAM_INVALID, scale
+    for scale in (2.0 ** 127, -2.0 ** 127, 0.0):  # (the missing workspace is found after the scale)
+        assert call(scale) == W.WQ_ERR_PARAM_NULLPTR, scale

@@ -52,7 +52,7 @@ int wq_tree_attention(const wq_tensor* q, const wq_tensor* k_cache, const wq_ten
   int st = wq::validate_tree(q, k_cache, v_cache, block_table, context_lens, q_starts, tree_mask, page_size, output,
                              &p);
   if (st != WQ_OK) return st;
-  if (!std::isfinite(scale)) return WQ_ERR_PARAM_INVALID;
+  if (!(std::fabs(scale) <= 0x1p127f)) return WQ_ERR_PARAM_INVALID;  // its product with log2(e) is finite
   const wq::TreePlan pl = wq::plan_tree(p);
   if ((st = check_workspace(workspace, workspace_size, pl.workspace)) != WQ_OK) return st;
   if (p.N == 0 || p.B == 0) return WQ_OK;
