@@ -103,8 +103,9 @@ int wq_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq
  * [q_starts[b], q_starts[b+1]), T_b of them, and the keys 0 .. context_lens[b] + T_b - 1; its
  * token i sees every key of the context and, of its own T_b tokens, those that its row of
  * tree_mask names.  Key j is row block_table[b, j / page_size] * page_size + j % page_size of
- * the caches.  A token that sees no key gives zeros.  What a token does not see has no part in
- * its result, NaN and infinities included.
+ * the caches.  A token that sees no key, or none whose score is above -inf, gives zeros.  What a
+ * token does not see has no part in its result, NaN and infinities included; what it sees has the part
+ * that the formula gives it, as far as its weight is above 0 in fp32.
  *
  *   q             required; WQ_F16 or WQ_BF16; rows (N, hq, d); d in {64, 128, 256}; N at most
  *                 2^24 and N * hq at most 2^30.

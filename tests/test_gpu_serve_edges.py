@@ -184,3 +184,81 @@ def test_lora_sums_that_a_factor_brings_back():
         c["b"] = (c["b"].sign() * 2.0 ** 127 * 1.5).to(torch.bfloat16)
         ref, bound = base.lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], None, c["x3"])
         close(base.lora_run(c), ref, bound, m)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("variant", VARIANTS, ids=VIDS)
+def test_tree_every_variant_where_nothing_is_seen(variant, dt):
+    """Empty rows of a mask, pages that do not exist, a table narrower than the context, scales of either sign and zero,
+    scores of -inf: in each kernel and head size."""
+    hq, hkv, d, tokens = variant
+    say("tree variants", variant, dt)
+    c = tree_case(151, dt, [(200, tokens), (60, tokens), (0, tokens)], hq, hkv, d, 16, "random", width=13)
+    c["mask"][1], c["mask"][2 * tokens + 1] = 0, 0
+    c["table"][0, 3], c["table"][1, 2] = -1, 10 ** 6
+    for scale in (None, 0.0, -0.3):
+        ref, bound = tree_ref(c, scale)
+        out = tree_run(c, scale=scale)
+        close(out, ref, bound, (variant, scale))
+        assert torch.equal(tree_run(c, scale=scale), out)
+    assert not out[2 * tokens + 1].any()
+    for key in range(60 + tokens):  # what the second sequence sees is -inf in one column that its queries multiply
+        slot = int(c["table"][1, key // 16]) * 16 + key % 16
+        if 0 <= slot < c["k"].shape[0]:
+            c["k"][slot, :, 7] = -math.inf
+    c["q"][:, :, 7] = 1.0
+    out = tree_run(c)
+    assert not out[tokens:2 * tokens].any() and torch.isfinite(out).all()
+    c["table"][:] = -1
+    assert not tree_run(c).any()
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("variant", VARIANTS, ids=VIDS)
+def test_tree_every_variant_unseen_values(variant, dt):
+    """NaN and infinities in K and V of drafted tokens that one token in turn sees."""
+    hq, hkv, d, tokens = variant
+    say("tree variants unseen", variant, dt)
+    nan, inf = math.nan, math.inf
+    c = tree_case(161, dt, [(70, tokens), (3, tokens)], hq, hkv, d, 16, "tree")
+    c["mask"][:] = torch.tensor([(1 << (i % tokens)) | 1 for i in range(2 * tokens)], device=DEV)[:, None]
+    clean = tree_run(c)
+    for b, ctx in enumerate((70, 3)):
+        one, two = (int(c["table"][b, (ctx + j) // 16]) * 16 + (ctx + j) % 16 for j in (1, 2))
+        c["v"][one, :, 3], c["v"][one, :, 5], c["v"][one, 0, d - 1] = nan, inf, -inf
+        c["k"][two], c["v"][two] = nan, inf
+    out = tree_run(c)
+    for i in range(2 * tokens):
+        if i % tokens == 1:
+            assert torch.isnan(out[i, :, 3]).all() and (out[i, :, 5] == inf).all()
+            assert (out[i, :hq // hkv, d - 1] == -inf).all() and torch.isfinite(out[i, :, 6:d - 1]).all()
+        elif i % tokens == 2:
+            assert torch.isnan(out[i]).all()
+        else:
+            assert torch.equal(out[i], clean[i])
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("lens,hq,hkv,d", [
+    ([(100, 200), (900, 1), (33, 1), (0, 1), (700, 2)], 8, 2, 64), ([(0, 300), (1000, 1), (50, 3)], 4, 4, 64),
+    ([(40, 90), (500, 1), (500, 1)], 8, 2, 128), ([(300, 150), (20, 1)], 6, 2, 128), ([(10, 70), (900, 1)], 4, 2, 256),
+    ([(500, 1)] * 40 + [(64, 64)], 4, 1, 128)])
+def test_tree_pieces_of_prompts_among_single_tokens(lens, hq, hkv, d, dt):
+    """Sequences of unlike token counts: one tile height, from the average, for all of them."""
+    say("tree unlike", str(lens)[:60], hq, hkv, d, dt)
+    for mask in (None, "tree"):
+        c = tree_case(171, dt, lens, hq, hkv, d, 16, mask)
+        ref, bound = tree_ref(c)
+        close(tree_run(c), ref, bound, mask)
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=IDS)
+@pytest.mark.parametrize("m,r,k,n", [(1, 16, 4096, 4096), (64, 32, 1024, 520), (777, 64, 512, 264), (3000, 72, 520, 136)])
+def test_lora_is_off_by_its_last_rounding(m, r, k, n, dt):
+    """In the root mean square, as for the attention: terms to 2^-16 (bf16) and 2^-22 (fp16) of the first product, and
+    sums of some thousand fp32 products, whose roundings add to a few 2^-22 of their size."""
+    say("lora rms", m, r, k, n, dt)
+    c = base.lora_case(181, dt, m, 4, r, k, n, order="mixed" if m > 1 else "one", x3=False)
+    ref, _ = base.lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], None, None)
+    rms = lambda x: float(x.square().mean().sqrt())
+    assert rms(base.lora_run(c).double() - ref) < 1.05 * rms(ref.to(dt).double() - ref)
