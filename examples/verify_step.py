@@ -43,7 +43,7 @@ class VerifyStep:
         self.heads, self.kv_heads, self.dim, self.page = heads, kv_heads, dim, page
         counts = [len(p) for p in parents]
         tokens = sum(counts)
-        count = max(adapters) + 1
+        count = max(max(adapters) + 1, 1)  # (one that nobody has, where nobody has any)
 
         # weights: int8 with a scale per column; adapters (rank, in) and (out, rank)
         codes = lambda k, n: torch.randint(-127, 128, (k, n), generator=g, dtype=torch.int8).to(device)

@@ -262,3 +262,16 @@ def test_lora_is_off_by_its_last_rounding(m, r, k, n, dt):
     ref, _ = base.lora_ref(c["x1"], c["a"], c["b"], c["indices"], c["scale"], None, None)
     rms = lambda x: float(x.square().mean().sqrt())
     assert rms(base.lora_run(c).double() - ref) < 1.05 * rms(ref.to(dt).double() - ref)
+
+
+def test_verify_step_without_adapters():
+    """The example's block where no request has an adapter."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from verify_step import VerifyStep
+    say("verify step without adapters")
+    step = VerifyStep([40, 3], [[-1, 0, 0], [-1]], [-1, -1])
+    want = step.plain()
+    got = step.step().double().cpu()
+    assert float((got - want).norm() / want.norm()) < 8 * 2.0 ** -9  # as in test_gpu_verify_step.py
