@@ -69,7 +69,7 @@ struct RopeProblem {
 };
 
 struct TreeProblem {
-  int64_t N = 0, B = 0, S = 0, pages = 0;
+  int64_t N = 0, B = 0, pages = 0;
   int32_t hq = 0, hkv = 0, group = 0, d = 0, width = 0, words = 0, page = 0;
   int32_t act = WQ_F16;
   int64_t q_t = 0, q_h = 0, k_t = 0, k_h = 0, v_t = 0, v_h = 0, o_t = 0, o_h = 0;

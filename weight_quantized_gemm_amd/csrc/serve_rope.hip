@@ -36,7 +36,7 @@ struct RopeArgs {
   int64_t q_t, q_h, k_t, k_h, v_t, v_h, qo_t, qo_h, ko_t, ko_h, vo_t, vo_h;
   int64_t T, S;
   int64_t block0;                  // the launch's first workgroup among all of the call's
-  int32_t hq, hkv, d, half;
+  int32_t hq, hkv, half;
   int32_t turn_units, head_units;  // units of a head: rotated ones, all of them
   int32_t units;                   // units of a token
   int32_t copy_units;              // units of a v head
@@ -44,8 +44,8 @@ struct RopeArgs {
   float factor;
 };
 
-// What a unit works on.  lo: its first element, within a head; hi: the element that turns with
-// it (half layout), or -1.  count: elements from lo on.
+// What a unit works on.  lo: its first element, within a head; pair: its first pair, if it turns
+// (otherwise it is copied).
 struct Unit {
   const uint16_t* src = nullptr;
   uint16_t* dst = nullptr;  // null: no unit, or a token whose slot drops it
@@ -194,7 +194,7 @@ hipError_t launch_rope(const RopeProblem& p, hipStream_t stream) {
   a.positions = p.positions; a.slots = p.slots; a.inv_freq = p.inv_freq;
   a.q_t = p.q_t; a.q_h = p.q_h; a.k_t = p.k_t; a.k_h = p.k_h; a.v_t = p.v_t; a.v_h = p.v_h;
   a.qo_t = p.qo_t; a.qo_h = p.qo_h; a.ko_t = p.ko_t; a.ko_h = p.ko_h; a.vo_t = p.vo_t; a.vo_h = p.vo_h;
-  a.T = p.T; a.S = p.S; a.hq = p.hq; a.hkv = p.hkv; a.d = p.d; a.half = p.half; a.factor = p.factor;
+  a.T = p.T; a.S = p.S; a.hq = p.hq; a.hkv = p.hkv; a.half = p.half; a.factor = p.factor;
   // 16-byte units where the rotated part is whole units: half layout, both halves start on one
   // and hold whole ones; interleaved, the rotated part ends on one.  Otherwise single pairs.
   const bool vec = p.interleaved ? p.half % 4 == 0 : p.half % 8 == 0;

@@ -78,7 +78,7 @@ struct TreeArgs {
   int64_t q_t, q_h, k_h, v_h, o_t, o_h;
   uint32_t k_row, v_row;  // bytes from one slot to the next
   int64_t pages, room;    // room: for this many cuts
-  int32_t N, B, hq, hkv, group, width, words, has_mask;
+  int32_t N, B, hkv, group, width, words, has_mask;
   int32_t blocks;     // workgroups of the launch
   int32_t R, unit;    // rows of a tile, keys of a unit
   FastDiv by_page, by_group;
@@ -959,7 +959,7 @@ hipError_t launch_tree(const TreeProblem& p, const TreePlan& pl, float scale, vo
   a.q_t = p.q_t; a.q_h = p.q_h; a.k_h = p.k_h; a.v_h = p.v_h;
   a.o_t = p.o_t; a.o_h = p.o_h;
   a.k_row = (uint32_t)(2 * p.k_t); a.v_row = (uint32_t)(2 * p.v_t);
-  a.pages = p.pages; a.room = pl.tiles; a.N = (int32_t)p.N; a.B = (int32_t)p.B; a.hq = p.hq; a.hkv = p.hkv; a.group = p.group;
+  a.pages = p.pages; a.room = pl.tiles; a.N = (int32_t)p.N; a.B = (int32_t)p.B; a.hkv = p.hkv; a.group = p.group;
   a.width = p.width; a.words = p.words; a.has_mask = p.has_mask; a.blocks = (int32_t)pl.blocks;
   a.by_page = fast_div((uint32_t)p.page); a.by_group = fast_div((uint32_t)p.group);
   a.scale = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;

@@ -298,7 +298,7 @@ int validate_tree(const wq_tensor* q, const wq_tensor* k_cache, const wq_tensor*
       if (starts_at(t, output->data)) return WQ_ERR_PARAM_INVALID;
 
   if (p) {
-    p->N = N; p->B = B; p->S = S; p->pages = S / page_size;
+    p->N = N; p->B = B; p->pages = S / page_size;
     p->hq = (int32_t)hq; p->hkv = (int32_t)hkv; p->group = (int32_t)(hq / hkv); p->d = (int32_t)d;
     p->width = (int32_t)width; p->page = (int32_t)page_size; p->act = act;
     p->q = q->data; p->q_t = stride_of(q, 0); p->q_h = stride_of(q, 1);
