@@ -41,11 +41,10 @@ LoraPlan plan_lora(const LoraProblem& p) {
     pl.workspace = align256(pl.list_bytes + (int64_t)pl.splits * p.m * p.r * 4);
     return pl;
   }
-  // k splits, a power of two, while workgroups are few: 4 of 64 tokens' windows, 2 of more, are
-  // counted for a window.  (All of them split in 8 instead: 13.2 us for 13.0 us at 64 tokens of 64
-  // adapters, 38.0 us for 36.4 us at 777 of 100 requests.)
+  // k splits, a power of two, while workgroups are few: 2 adapters are counted for a window, so that up to 64
+  // tokens have all 8.  (8 for more tokens instead of what is counted: 38.0 us for 36.4 us at 777 of 100 requests.)
   const int64_t most = ceil_div(p.k, 256);
-  const int64_t items = pl.windows * (p.m <= 64 ? std::min<int64_t>(4, pl.slots) : 2) * pl.rank_blocks;
+  const int64_t items = pl.windows * 2 * pl.rank_blocks;
   while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && 2 * items * pl.splits <= 2 * kCUs) pl.splits *= 2;
   pl.kchunk = (int)(ceil_div(ceil_div(p.k, pl.splits), 64) * 64);
   pl.splits = (int)ceil_div(p.k, pl.kchunk);
