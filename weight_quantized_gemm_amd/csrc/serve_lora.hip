@@ -470,9 +470,10 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
     if (!busy) return;
 
     // Of 8 columns of a row, those whose sums are not finite, summed anew in fp32 from h itself: against an infinity in B,
-    // terms of unlike signs or a zero one make a NaN, and a row's factor may bring back what passed fp32.
-    auto sum_apart = [&](float (&v)[8], int64_t row, int64_t n) {
-      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // terms of unlike signs or a zero one make a NaN, and a row's factor may bring back what passed fp32.  The
+    // row's factor f is in all of them then, and 1 afterwards.
+    auto sum_apart = [&](float (&y)[8], float& f, int64_t row, int64_t n) {
+      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
       for (int r = 0; r < rank; ++r) {
         const int parts = parts_of(r / RB);
@@ -481,11 +482,11 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
         for (int z = 0; z < parts; ++z) h += p.h[(z * p.m + row) * p.r + r];
         h *= it.scale;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(h, act_to_f32<BF16>(bk[(n + i) * p.r + r]), y[i]);
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(h, act_to_f32<BF16>(bk[(n + i) * p.r + r]), s[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!__builtin_isfinite(v[i])) v[i] = y[i];
+      for (int i = 0; i < 8; ++i) y[i] = __builtin_isfinite(y[i]) ? f * y[i] : s[i];
+      f = 1.f;
     };
 
     f32x4_t acc[2][MT];
@@ -550,20 +551,16 @@ __global__ __launch_bounds__(256, W == 64 ? 2 : CH == 8 ? 3 : 4) void lora_expan
           __builtin_amdgcn_wave_barrier();
           const f32x4_t y0 = *(const f32x4_t*)(sums + row4 * kSumRow + col4);
           const f32x4_t y1 = *(const f32x4_t*)(sums + row4 * kSumRow + col4 + 4);
-          const float f = factor[16 * t + row4];
-          float v[8], z = 0.f;
+          float f = factor[16 * t + row4], z = 0.f;
+          float y[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float y = i < 4 ? y0[i] : y1[i - 4];
-            v[i] = f * y;
-            z = fmaf(y, 0.f, z);
-          }
+          for (int i = 0; i < 8; ++i) z = fmaf(y[i], 0.f, z);
           const int wr = 16 * t + row4;
-          if (z != 0.f && ((rows >> wr) & 1) && nc + col4 < n1) sum_apart(v, w0 + wr, nc + col4);
+          if (z != 0.f && ((rows >> wr) & 1) && nc + col4 < n1) sum_apart(y, f, w0 + wr, nc + col4);
 #pragma unroll
           for (int d = 0; d < 4; ++d)
-            o[t][d] = pack2<BF16>(act_to_f32<BF16>((uint16_t)o[t][d]) + v[2 * d],
-                                  act_to_f32<BF16>((uint16_t)(o[t][d] >> 16)) + v[2 * d + 1]);
+            o[t][d] = pack2<BF16>(act_to_f32<BF16>((uint16_t)o[t][d]) + f * y[2 * d],
+                                  act_to_f32<BF16>((uint16_t)(o[t][d] >> 16)) + f * y[2 * d + 1]);
           __builtin_amdgcn_wave_barrier();
         }
       }
