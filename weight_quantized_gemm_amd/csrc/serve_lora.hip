@@ -26,14 +26,15 @@
 //    that follow each other hold different rows, every lane is an access of its own: 389 us
 //    instead of 125 us without the loads of B, for 16384 tokens x 8192 columns at rank 64.
 //
-// Measured (bf16, MI355X, a call with both products):
-//   1 token, rank 16, k = n = 4096: 8.5 us, of which the kernels take 3.0 and 4.7 us: two launches
-//     and the chain index -> rank -> operands -> sum in each;
-//   64 tokens of 32 adapters, rank 32, k = n = 8192 (fp16): 18.5 us for 26.8 MB, kernels 8.4 and
-//     11.4 us (1.0 and 1.6 TB/s): a workgroup lives for four rounds of loads and its launch and
+// Measured (bf16, MI355X, a call with both products; kernels: medians under a tracer, which makes each a
+// little longer):
+//   1 token, rank 16, k = n = 4096: 8.9 us; kernels 3.8 and 5.3 us: two launches and the chain index ->
+//     rank -> operands -> sum in each;
+//   64 tokens of 32 adapters, rank 32, k = n = 8192 (fp16): 18.9 us for 26.8 MB; kernels 8.1 and
+//     11.4 us: a workgroup lives for four rounds of loads, one stage ahead, and its launch and
 //     start take as long as those;
-//   16384 tokens of 8 adapters, rank 64, k = 4096, n = 8192: 201 us for 669 MB (3.3 TB/s; a copy runs at
-//     5.2); 5 us the list, 51 us the first product (2.6 TB/s of x1), 144 us the second (3.7 TB/s: x3
+//   16384 tokens of 8 adapters, rank 64, k = 4096, n = 8192: 205 us for 669 MB (3.3 TB/s; a copy runs at
+//     5.2); 5 us the list, 49 us the first product (2.7 TB/s of x1), 156 us the second (3.4 TB/s: x3
 //     and out through LDS, between loads of B that stand in the same queue).
 #include <algorithm>
 

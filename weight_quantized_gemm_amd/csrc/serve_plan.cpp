@@ -23,10 +23,10 @@ LoraPlan plan_lora(const LoraProblem& p) {
   pl.windows = ceil_div(p.m, pl.window);
   // Side-by-side work items of a 16-row window, whose rows may each have an adapter of their own:
   // all of them where there are few windows, otherwise 4, since most workgroups of more would find
-  // nothing.  16 against 4 of them: 13.1 us and 19.7 us for 64 tokens of 64 adapters (rank 16, k = n =
-  // 4096), 26.4 us and 22.5 us for 128 tokens of 64, 45 us and 36 us for 777 tokens of 100 requests.
+  // nothing.  16 against 4 of them: 13.3 us and 20.1 us for 64 tokens of 64 adapters (rank 16, k = n =
+  // 4096), 26.8 us and 23.2 us for 128 tokens of 64, 46 us and 37 us for 777 tokens of 100 requests.
   // Only where most rows of many windows differ does that rule lose (1500 tokens of 1500 requests
-  // and 32 adapters: 83 us and 91 us), which the shapes do not tell.
+  // and 32 adapters: 87 us and 94 us), which the shapes do not tell.
   const int64_t distinct = std::min<int64_t>({p.L + 1, p.m, pl.window});
   if (pl.window == 16) pl.slots = (int)std::min<int64_t>(distinct, p.m <= 64 ? 16 : 4);
   pl.rank_tiles = p.r <= 16 ? 1 : p.r <= 32 ? 2 : kLoraRankTiles;
@@ -42,7 +42,7 @@ LoraPlan plan_lora(const LoraProblem& p) {
     return pl;
   }
   // k splits, a power of two, while workgroups are few: 2 adapters are counted for a window, so that up to 64
-  // tokens have all 8.  (8 for more tokens instead of what is counted: 38.0 us for 36.4 us at 777 of 100 requests.)
+  // tokens have all 8.  (8 for more tokens instead of what is counted: 38.9 us for 37.3 us at 777 of 100 requests.)
   const int64_t most = ceil_div(p.k, 256);
   const int64_t items = pl.windows * 2 * pl.rank_blocks;
   while (2 * pl.splits <= std::min<int64_t>(kLoraSplits, most) && 2 * items * pl.splits <= 2 * kCUs) pl.splits *= 2;

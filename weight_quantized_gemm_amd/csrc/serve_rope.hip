@@ -14,9 +14,10 @@
 // ulp is 1/128 radian), so the product is taken in fp64 in turns, reduced to half a turn
 // there, and only the remainder is fp32.
 //
-// Measured (MI355X): 16384 tokens, 32 + 8 + 8 heads of 128, bf16: 76.5 us for 403 MB, 5.26 TB/s, the rate of
-// a large copy; 509 tokens (25 MB): 6.6 us, 3.8 TB/s; 4 tokens: 5.0 us, of which the kernel takes 3.0
-// and the rest is the launch.
+// Measured (MI355X): 16384 tokens, 32 + 8 + 8 heads of 128, bf16: 76.2 us for 403 MB, 5.28 TB/s, the rate of
+// a large copy; 509 tokens (25 MB): 6.6 us, 3.8 TB/s; 4 tokens: 5.2 us, of which the kernel takes 3.2
+// and the rest is the launch.  Where the rotated part is not whole 16-byte units, a unit is a pair of 2-byte
+// elements: 378 us for the same tokens with 20 elements rotated, 1.07 TB/s.
 #include <algorithm>
 
 #include "serve_device.h"

@@ -7,9 +7,9 @@ namespace wq {
 
 // ---- adapters
 // Up to here a window is 16 token rows, beyond 64: short windows need no list and no tokens side by
-// side with one adapter, long ones read an adapter less often.  16 and 64 rows, bf16, k = n = 4096: 27.0 us and
-// 36.6 us for 1100 tokens of 4 requests, 69 us and 49 us for 3000 of 20, 118 us and 74 us for
-// 4096 of 100; k = n = 8192, 2048 tokens of 200 requests: 107 us and 123 us.
+// side with one adapter, long ones read an adapter less often.  16 and 64 rows, bf16, rank 64, k = n = 4096: 27.4 us
+// and 36.8 us for 1100 tokens of 4 requests, 87 us and 52 us for 3000 of 20, 145 us and 82 us for
+// 4096 of 100; k = n = 8192, 2048 tokens of 200 requests: 126 us and 136 us.
 constexpr int64_t kLoraSmallM = 2048;
 constexpr int kLoraRankTiles = 4;      // most 16-rank tiles of one workgroup of the first product
 constexpr int kLoraCols = 128;         // columns of one round of the second product's workgroups

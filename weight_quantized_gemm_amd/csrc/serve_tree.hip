@@ -35,20 +35,20 @@
 // enters the second product as two 16-bit terms, itself rounded and what the rounding left, for an error of at most
 // 2^-16 (bf16) or 2^-22 (fp16) of it, and in fp16 2^-32 of the largest, less than the sums' own
 // rounding.  One term would be off by as much as the result's last rounding is; the second costs nothing where
-// memory bounds the kernel, and up to 28 % where the matrix cores do (512 rows: 240 -> 305 us).  The sums
+// memory bounds the kernel, and up to 28 % where the matrix cores do (512 rows: 238 us without it, 300 us).  The sums
 // are taken of the same two terms, by the matrix cores (against ones), so that the weights add up to 1 exactly.
 //
 // Measured (MI355X, both kernels of a call):
-//   64 single tokens over 16 to 8192 keys, 8 cached heads of 128, fp16: 248 us for 1.36 GB, 5.5 TB/s; reads
+//   64 single tokens over 2144 to 8192 keys, 8 cached heads of 128, fp16: 249 us for 1.36 GB, 5.4 TB/s; reads
 //     of 256-byte pieces 2 KB apart, which a cache of 8 heads is made of, reach 6.1 TB/s with no
 //     arithmetic at all;
-//   one token over 4020 keys (4.1 MB): 12.7 us, 9.3 + 3.1 us in the kernels: launches and the chain
-//     length -> page -> key -> score -> join;
-//   8 sequences of 64 drafted tokens, 64 query heads for 8 cached ones of 128, bf16: 236 us,
-//     765 TFLOP/s of the 1215 that a large product reaches.  The matrix cores are busy for 37 % of
-//     the cycles, the vector units for 41 % (exponentials, packing, addresses), LDS for 19 %
-//     without bank conflicts: what is lost is that the two waves of a SIMD, held together by the
-//     shared tiles, do the same thing at the same time.
+//   one token over 1001 keys (4.1 MB): 13.1 us: two launches and the chain length -> page -> key ->
+//     score -> join, in about 64 workgroups of 128 keys;
+//   8 sequences of 60 to 64 drafted tokens over 5632 to 16384 keys, 64 query heads for 8 cached ones of 128,
+//     bf16: 300 us, 600 TFLOP/s of the formula's products and 900 with those of the second terms, of the 1215
+//     that a large product reaches.  The matrix cores are busy for 48 % of the cycles, the vector units for
+//     47 % (exponentials, packing, addresses), LDS for 16 % without bank conflicts: what is lost
+//     is that the two waves of a SIMD, held together by the shared tiles, do the same thing at the same time.
 #include <algorithm>
 #include <cmath>
 
@@ -359,7 +359,7 @@ __device__ __forceinline__ bool compute_rows(const TreeArgs& a, const Seq& s, co
     }
 
   // vector instructions first: the other wave of the SIMD is then sooner at its matrix products
-  // (512 rows: 243 -> 238 us)
+  // (512 rows, before the weights' second terms: 243 -> 238 us)
   if constexpr (!SLOW) __builtin_amdgcn_s_setprio(1);
   uint32_t seen[NT][KT / 32];  // SLOW: bit r of word b, whether this lane's row sees key 32 b + r
   if constexpr (SLOW) {
