@@ -20,6 +20,13 @@ is in ``serve.py`` and reached from here too:
     rope:              rotary positions of q and k; k and v to rows of a cache
     tree_attention:    attention of one, a chain or a tree of new tokens over a paged cache
 
+and in ``step.py`` what a step needs around its attention:
+
+    step_layout:       starts, positions, cache rows, masks and new pages from the requests' lengths
+    norm_rope:         rope with norms of the heads and positions of several axes
+    prefix_attention:  tree_attention of sequences that share long prefixes
+    verify_drafts:     the drafted tokens that the target accepts, and the one that follows
+
 (the formulas of the aclnnWeightQuantMatmulAllReduce guide, section 计算公式, and of the
 aclnnQuantMatmulAllReduceV2 page, section Function, at one rank).
 """
@@ -37,7 +44,9 @@ __all__ = ["WQ_F16", "WQ_BF16", "WQ_F32", "WQ_I8", "WQ_I4", "WQ_I32", "WQ_F8E4M3
            "antiquant_workspace_size", "quant_matmul", "quant_workspace_size", "AntiquantMatmul",
            "QuantMatmul", "profile_next_call", "EXPORTS",
            "SERVE_EXPORTS", "WQ_ROPE_HALF", "WQ_ROPE_INTERLEAVED", "LoraMatmul", "lora_matmul", "Rope", "rope",
-           "rope_frequencies", "TreeAttention", "tree_attention", "tree_mask_from_parents"]
+           "rope_frequencies", "TreeAttention", "tree_attention", "tree_mask_from_parents",
+           "StepTables", "StepLayout", "step_layout", "NormRope", "norm_rope", "rope_axes", "PrefixAttention",
+           "prefix_attention", "VerifyDrafts", "verify_drafts"]
 
 WQ_F16, WQ_BF16, WQ_F32, WQ_I8, WQ_I4, WQ_I32, WQ_F8E4M3 = 1, 2, 3, 4, 5, 6, 7
 WQ_OK, WQ_ERR_PARAM_NULLPTR, WQ_ERR_PARAM_INVALID, WQ_ERR_RUNTIME = 0, 161001, 161002, 561001
@@ -91,6 +100,14 @@ def declare(L):
         "wq_tree_attention_get_workspace_size": ([P] * 7 + [ctypes.c_int64, P, u64p], ctypes.c_int),
         "wq_tree_attention": ([P] * 7 + [ctypes.c_int64, ctypes.c_float, P, ctypes.c_void_p, ctypes.c_uint64,
                                          ctypes.c_void_p], ctypes.c_int),
+        "wq_norm_rope": ([P] * 8 + [ctypes.c_float, P, ctypes.c_int32, ctypes.c_float] + [P] * 3 + [ctypes.c_void_p],
+                         ctypes.c_int),
+        "wq_step_layout": ([P] * 7 + [ctypes.c_int64] + [P] * 6 + [ctypes.c_void_p], ctypes.c_int),
+        "wq_prefix_attention_get_workspace_size": ([P] * 10 + [ctypes.c_int64, P, u64p], ctypes.c_int),
+        "wq_prefix_attention": ([P] * 10 + [ctypes.c_int64, ctypes.c_float, P, ctypes.c_void_p, ctypes.c_uint64,
+                                            ctypes.c_void_p], ctypes.c_int),
+        "wq_verify_drafts_get_workspace_size": ([P] * 10 + [u64p], ctypes.c_int),
+        "wq_verify_drafts": ([P] * 10 + [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p], ctypes.c_int),
     }
     for name, (args, res) in sigs.items():
         if hasattr(L, name):
@@ -405,3 +422,5 @@ def quant_matmul(x1, x2, dequant_scale, pertoken_scale=None, bias=None, x3=None,
 from .serve import (SERVE_EXPORTS, WQ_ROPE_HALF, WQ_ROPE_INTERLEAVED, LoraMatmul, Rope,  # noqa: E402
                     TreeAttention, lora_matmul, rope, rope_frequencies, tree_attention,
                     tree_mask_from_parents)
+from .step import (NormRope, PrefixAttention, StepLayout, StepTables, VerifyDrafts, norm_rope,  # noqa: E402
+                   prefix_attention, rope_axes, step_layout, verify_drafts)

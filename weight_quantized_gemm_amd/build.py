@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["aq_gemm_int8.hip", "aq_gemm_int4.hip", "aq_gemm_fp8.hip", "qm_gemm.hip",
            "aq_smallm.hip", "aq_prep.hip", "wq_noalloc.hip", "wq_validate.cpp", "wq_plan.cpp", "wq_api.cpp",
            "serve_lora.hip", "serve_rope.hip", "serve_tree.hip", "serve_validate.cpp", "serve_plan.cpp",
-           "serve_api.cpp"]
+           "serve_api.cpp", "serve_layout.hip", "serve_norm_rope.hip", "serve_prefix.hip", "serve_verify.hip",
+           "serve_step_validate.cpp", "serve_step_plan.cpp", "serve_step_api.cpp"]
 ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", f"-I{INCLUDE}", f"-I{CSRC}"]
 DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -1,0 +1,48 @@
+// Planning of the serving operators around a step's attention: splits and workspaces.  Host-only C++; like
+// serve_plan.cpp the plans depend on shapes alone.
+#include <algorithm>
+
+#include "serve_step.h"
+#include "serve_tile.h"
+
+namespace wq {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+PrefixPlan plan_prefix(const PrefixProblem& p) {
+  PrefixPlan pl;
+  if (p.own.N == 0 || p.own.B == 0) return pl;
+  pl.own = plan_tree(p.own);
+  pl.shared = plan_tree(p.shared);  // without prefixes: nothing
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) { const int64_t here = at; at += align256(bytes); return here; };
+  auto parts = [&](const TreePlan& t) { return (2 * t.blocks + t.tiles) * t.rows * (int64_t)(p.own.d + 2) * 4; };
+  pl.shared_notes = take(pl.shared.notes_bytes);
+  pl.own_notes = take(pl.own.notes_bytes);
+  pl.groups = take(p.shared.B * kPrefixGroupBytes);
+  pl.shared_parts = take(parts(pl.shared));
+  pl.own_parts = take(parts(pl.own));
+  pl.workspace = at;
+  return pl;
+}
+
+VerifyPlan plan_verify(const VerifyProblem& p) {
+  VerifyPlan pl;
+  if (p.B == 0) return pl;
+  // A request's row is cut into chunks of whole kVerifyStep probabilities, as many as give about four workgroups
+  // to each of 256 compute units, and no more than one step each needs.
+  const int64_t steps = ceil_div(p.V, kVerifyStep);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(steps, ceil_div(4 * 256, p.B)));
+  pl.chunk = ceil_div(steps, want) * kVerifyStep;
+  pl.chunks = ceil_div(p.V, pl.chunk);
+  pl.sums = align256(p.B * kVerifyStateBytes);
+  pl.refused = pl.sums + align256(p.B * pl.chunks * 16);
+  pl.workspace = pl.refused + align256(p.N * 8);
+  return pl;
+}
+
+}  // namespace wq

@@ -22,4 +22,10 @@ constexpr int tree_key_waves(int d) { return d == 256 ? 2 : 4; }   // waves that
 constexpr int kTreeCutBytes = 32;      // what is noted of a tile for the join
 constexpr int tree_row_keys(int waves) { return waves == 2 ? 32 : 64; }  // keys of a tile whose rows the waves split
 
+// ---- shared prefixes
+constexpr int kPrefixGroupBytes = 16;  // what is noted of a group for the join
+
+// ---- verification
+constexpr int kVerifyStep = 1024;  // probabilities that a workgroup of the sums takes at a time
+
 }  // namespace wq

@@ -19,7 +19,9 @@ import math
 from . import (_alloc_on, _check, _desc, _ref, _stream_handle, _torch, lib)
 
 SERVE_EXPORTS = ("wq_lora_matmul_get_workspace_size", "wq_lora_matmul", "wq_rope",
-                 "wq_tree_attention_get_workspace_size", "wq_tree_attention")
+                 "wq_tree_attention_get_workspace_size", "wq_tree_attention", "wq_norm_rope", "wq_step_layout",
+                 "wq_prefix_attention_get_workspace_size", "wq_prefix_attention",
+                 "wq_verify_drafts_get_workspace_size", "wq_verify_drafts")
 WQ_ROPE_HALF, WQ_ROPE_INTERLEAVED = 0, 1
 
 
