@@ -154,7 +154,7 @@ int wq_tree_attention(const wq_tensor* q, const wq_tensor* k_cache, const wq_ten
  *              not turn (its position is 0).  Required with positions of two dimensions.
  *   q_weight   optional; q's dtype or WQ_F32; (d).  Absent: q is not normed.
  *   k_weight   optional (only with k); the same for k.
- *   eps        finite and above 0.
+ *   eps        finite and at least 2^-126.
  * Sums are fp32 and do not overflow: a head whose squares pass fp32 is taken with a factor.
  */
 int wq_norm_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, const wq_tensor* positions,

@@ -33,14 +33,14 @@ PrefixPlan plan_prefix(const PrefixProblem& p) {
 VerifyPlan plan_verify(const VerifyProblem& p) {
   VerifyPlan pl;
   if (p.B == 0) return pl;
-  // A request's row is cut into chunks of whole kVerifyStep probabilities, as many as give about four workgroups
-  // to each of 256 compute units, and no more than one step each needs.
-  const int64_t steps = ceil_div(p.V, kVerifyStep);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(steps, ceil_div(4 * 256, p.B)));
-  pl.chunk = ceil_div(steps, want) * kVerifyStep;
-  pl.chunks = ceil_div(p.V, pl.chunk);
+  pl.unit = ceil_div(p.V, (int64_t)kVerifyUnits * kVerifyStep) * kVerifyStep;
+  pl.units = ceil_div(p.V, pl.unit);
+  // Workgroups of four waves: as many as give each of 256 compute units about eight, and a wave at least one unit.
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(pl.units, 4), ceil_div(8 * 256, p.B)));
+  pl.chunk = ceil_div(ceil_div(pl.units, want), 4) * 4;
+  pl.chunks = ceil_div(pl.units, pl.chunk);
   pl.sums = align256(p.B * kVerifyStateBytes);
-  pl.refused = pl.sums + align256(p.B * pl.chunks * 16);
+  pl.refused = pl.sums + align256(p.B * pl.units * 8);
   pl.workspace = pl.refused + align256(p.N * 8);
   return pl;
 }

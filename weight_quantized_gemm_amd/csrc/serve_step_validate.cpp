@@ -1,6 +1,7 @@
 // Argument checks of the serving operators around a step's attention, in the library's order (null
 // pointers, dtypes, attributes, shapes and layout), and their size queries.  Pure host C++; no device
 // is touched.
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -33,7 +34,7 @@ int validate_norm_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* 
   if (axes && axes->dtype != WQ_I32) return WQ_ERR_PARAM_INVALID;
   for (const wq_tensor* t : {q_weight, k_weight})
     if (t && t->dtype != q->dtype && t->dtype != WQ_F32) return WQ_ERR_PARAM_INVALID;
-  if (!std::isfinite(eps) || !(eps > 0.f) || (k_weight && !k)) return WQ_ERR_PARAM_INVALID;
+  if (!std::isfinite(eps) || !(eps >= FLT_MIN) || (k_weight && !k)) return WQ_ERR_PARAM_INVALID;
 
   if (!dims_ok(positions, 1, 2)) return WQ_ERR_PARAM_INVALID;
   if (positions->ndim == 2 && (!axes || positions->shape[0] < 1 || positions->shape[0] > 16 || !contiguous(positions)))

@@ -26,6 +26,7 @@ constexpr int tree_row_keys(int waves) { return waves == 2 ? 32 : 64; }  // keys
 constexpr int kPrefixGroupBytes = 16;  // what is noted of a group for the join
 
 // ---- verification
-constexpr int kVerifyStep = 1024;  // probabilities that a workgroup of the sums takes at a time
+constexpr int kVerifyStep = 512;    // probabilities that a wave takes at a time
+constexpr int kVerifyUnits = 1024;  // most sums of a row
 
 }  // namespace wq

@@ -6,9 +6,10 @@
 // whose running sum passes u times the whole.
 //
 //   sums: each workgroup has a chunk of a request's row.  It walks through the tests itself (the wave's lanes hold
-//     the tokens, so that a step is a ballot), which takes less than a launch of its own, and sums its
-//     chunk of r, and of p, which stands for r where nothing is left of that.
-//   pick: a workgroup for each request finds the chunk that the random share falls into and the token in it.
+//     the tokens, so that a step is a ballot), which takes less than a launch of its own, and its waves sum
+//     r over units of 512 elements in a row (more where a row would have over 1024 units).
+//   pick: a workgroup for each request finds the unit that the random share falls into, and a wave the
+//     token in it.  Where nothing is left of r it sums the units of p first.
 //
 // Where drafts of a tree have probabilities, the second child of a token is tested against what the first left,
 // divided by its sum: a row to be summed in the middle of the walk.  There a workgroup for each request walks
@@ -26,8 +27,8 @@
 namespace wq {
 namespace {
 
-constexpr int kThreads = 256;       // of the sums
-constexpr int kWide = 1024;         // of the pick and the walk of its own
+constexpr int kThreads = 256;       // of the sums and the pick
+constexpr int kWide = 1024;         // of the walk of its own
 constexpr int kMaxTokens = kVerifyTokens;
 
 struct State {
@@ -43,11 +44,11 @@ struct VerifyArgs {
   const float *accept, *sample;
   int32_t *accepted, *counts, *next;
   State* state;
-  double* sums;      // (of r, of p) of each request's chunks
+  double* sums;      // of each request's units
   double* scales;    // with draft: a request's refusals' sums, from its first row on
   int32_t* refused;  // without: the refused tokens
   int64_t t_row, d_row;
-  int32_t N, V, depth, chunk, chunks;
+  int32_t N, V, depth, unit, units, chunk;
 };
 
 enum Kind { kF32, kF16, kBf16 };
@@ -59,6 +60,29 @@ __device__ __forceinline__ float value(const void* base, int64_t i) {
 }
 // A probability: negative numbers and NaN are 0.
 __device__ __forceinline__ double prob(float v) { return (double)fmaxf(v, 0.f); }
+
+// What another lane of the wave has, by a data-parallel move (0 where there is none).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  const i32x2_t x = __builtin_bit_cast(i32x2_t, v);
+  return __builtin_bit_cast(double, i32x2_t{__builtin_amdgcn_update_dpp(0, x[0], CTRL, ROWS, 0xf, false),
+                                            __builtin_amdgcn_update_dpp(0, x[1], CTRL, ROWS, 0xf, false)});
+}
+// The sum of lanes 0 .. this one: within rows of 16, then from row to row.
+__device__ __forceinline__ double wave_upto(double v) {
+  v += moved<0x111, 0xf>(v);
+  v += moved<0x112, 0xf>(v);
+  v += moved<0x114, 0xf>(v);
+  v += moved<0x118, 0xf>(v);
+  v += moved<0x142, 0xa>(v);         // lane 15 of rows 0 and 2 to rows 1 and 3
+  return v + moved<0x143, 0xc>(v);   // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ double lane_before(double v) { return moved<0x138, 0xf>(v); }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const i32x2_t x = __builtin_bit_cast(i32x2_t, v);
+  return __builtin_bit_cast(double, i32x2_t{__builtin_amdgcn_readlane(x[0], lane), __builtin_amdgcn_readlane(x[1], lane)});
+}
+__device__ __forceinline__ double wave_total(double v) { return lane_of(wave_upto(v), 63); }
 
 struct Rows {
   int q0 = 0, n = 0;  // first row, tokens looked at
@@ -77,8 +101,6 @@ struct Walk {
   int token[kMaxTokens];      // the refused ones (without draft)
   double scale[kMaxTokens];   // the sums that refusals left (trees with draft)
 };
-
-__device__ __forceinline__ double shuffled(double v, int lane) { return __shfl(v, lane, 64); }
 
 // The tests of a request's tokens by one wave; `again`(row, refusals): the scale of one more refusal, where the
 // next child needs it (trees with draft; all threads of the workgroup take part).
@@ -118,9 +140,9 @@ __device__ void walk_tests(const VerifyArgs& a, const Rows& r, int lane, Walk& w
       if (!next) break;
       const int at = __builtin_ctzll(next);
       from = base + at + 1;
-      const int x = __shfl(token, at, 64);
-      const double ux = (double)__shfl(u, at, 64), qx = shuffled(q, at);
-      double px = shuffled(p, at);
+      const int x = __builtin_amdgcn_readlane(token, at);
+      const double ux = (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(u), at)), qx = lane_of(q, at);
+      double px = lane_of(p, at);
       if (!a.draft) {  // a sibling of the same token that was refused has taken it all
         bool same = false;
         for (int i = lane; i < refused; i += 64) same |= w.token[i] == x;
@@ -175,12 +197,6 @@ __device__ __forceinline__ void load8(const void* base, int64_t row, int v, int 
   for (int i = 0; i < 8; ++i) f[i] = v + i < end ? value<KIND>(base, row + v + i) : 0.f;
 }
 
-__device__ __forceinline__ double wave_total(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
 // What is left of a row at the 8 elements from v on; list: the refused tokens (without draft) of this chunk.
 struct Left {
   const double* scale = nullptr;
@@ -204,6 +220,24 @@ __device__ __forceinline__ void left8(const float* pf, const float* qf, bool dra
         if (in == (uint32_t)i) r[i] = 0.0;
     }
   }
+}
+
+// The sum of what is left over a unit, by a wave.
+template <int KIND, bool DRAFT>
+__device__ __forceinline__ double unit_sum(const VerifyArgs& a, int64_t at_t, int64_t at_d, const Left& l, int u, int lane) {
+  const int lo = u * a.unit, hi = (int)min((int64_t)lo + a.unit, (int64_t)a.V);
+  const bool draft = DRAFT && l.refused > 0;  // without a refusal p is all that is read
+  double sum = 0.0;
+  for (int v = lo + 8 * lane; v < hi; v += kVerifyStep) {
+    float pf[8], qf[8];
+    double x[8];
+    load8<KIND>(a.target, at_t, v, hi, pf);
+    if (draft) load8<KIND>(a.draft, at_d, v, hi, qf);
+    left8(pf, qf, draft, l, v, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += x[i];
+  }
+  return wave_total(sum);
 }
 
 // The refused tokens of elements [lo, hi) among `count`, into LDS by all threads.
@@ -280,8 +314,7 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(const VerifyArgs 
   __shared__ Walk w;
   __shared__ int list[kMaxTokens];
   __shared__ int listed;
-  __shared__ double waves[kThreads / 64][2];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.y, chunk = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), b = blockIdx.y, chunk = blockIdx.x;
   const Rows r = request(a, b);
   if (tid == 0) listed = 0;
   if constexpr (WALKED) {
@@ -304,129 +337,119 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(const VerifyArgs 
   }
   if (w.row < 0) return;
 
-  const int lo = chunk * a.chunk, hi = min(lo + a.chunk, a.V);
+  const int u0 = chunk * a.chunk, u1 = min(u0 + a.chunk, a.units);
   Left l;
   l.scale = w.scale;
   l.list = list;
   l.refused = uniform(w.refused);
   if (!DRAFT) {
-    pick_listed(w.token, l.refused, lo, hi, list, &listed, tid, kThreads);
+    const int64_t lo = (int64_t)u0 * a.unit, hi = (int64_t)u1 * a.unit;
+    pick_listed(w.token, l.refused, (int)lo, (int)min(hi, (int64_t)a.V), list, &listed, tid, kThreads);
     __syncthreads();
     l.listed = uniform(listed);
   }
   const int64_t at_t = (int64_t)w.row * a.t_row, at_d = (int64_t)w.row * a.d_row;
-  const bool draft = DRAFT && l.refused > 0;  // without a refusal p is all that is read
-  double left = 0.0, whole = 0.0;
-#pragma unroll 2
-  for (int v = lo + 8 * tid; v < hi; v += 8 * kThreads) {
-    float pf[8], qf[8];
-    double x[8];
-    load8<KIND>(a.target, at_t, v, hi, pf);
-    if (draft) load8<KIND>(a.draft, at_d, v, hi, qf);
-    left8(pf, qf, draft, l, v, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      left += x[i];
-      whole += prob(pf[i]);
-    }
-  }
-  left = wave_total(left);
-  whole = wave_total(whole);
-  if (lane == 0) waves[wave][0] = left, waves[wave][1] = whole;
-  __syncthreads();
-  if (tid == 0) {
-    left = whole = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) left += waves[i][0], whole += waves[i][1];
-    double* to = a.sums + ((int64_t)b * a.chunks + chunk) * 2;
-    to[0] = left;
-    to[1] = whole;
+  double* sums = a.sums + (int64_t)b * a.units;
+  for (int u = u0 + wave; u < u1; u += kThreads / 64) {
+    const double sum = unit_sum<KIND, DRAFT>(a, at_t, at_d, l, u, lane);
+    if (lane == 63) sums[u] = sum;
   }
 }
 
 // ------------------------------------------------------------------------------ the token
-// What stands before this thread of a sum over the workgroup's threads, in their order.
-__device__ __forceinline__ double before(double v, double* waves, int tid) {
-  const int lane = tid & 63, wave = tid >> 6;
-  double upto = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double t = __shfl_up(upto, o, 64);
-    if (lane >= o) upto += t;
-  }
-  __syncthreads();
-  if (lane == 63) waves[wave] = upto;
-  __syncthreads();
-  double sum = 0.0;
-  for (int w = 0; w < wave; ++w) sum += waves[w];
-  const double prior = __shfl_up(upto, 1, 64);
-  return sum + (lane ? prior : 0.0);
-}
-
 template <int KIND, bool DRAFT>
-__global__ __launch_bounds__(kWide) void verify_pick_kernel(const VerifyArgs a) {
+__global__ __launch_bounds__(kThreads) void verify_pick_kernel(const VerifyArgs a) {
   __shared__ double scale[kMaxTokens];
   __shared__ int list[kMaxTokens];
   __shared__ int listed, found, last;
-  __shared__ double waves[kWide / 64], total[2], base_of;
-  const int tid = threadIdx.x, b = blockIdx.x;
+  __shared__ double waves[kThreads / 64], base_of;
+  constexpr int kPer = kVerifyUnits / kThreads;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), b = blockIdx.x;
   const Rows r = request(a, b);
   const State s = a.state[b];
   if (s.row < 0) {
     if (tid == 0) a.next[b] = -1;
     return;
   }
-  if (tid == 0) {
-    listed = 0;
-    found = a.chunks;
-    last = -1;
-  }
-  if (DRAFT && a.parents)
-    for (int i = tid; i < s.refused - 1; i += kWide) scale[i] = a.scales[r.q0 + i];
-
-  // the chunk: there are at most kWide, one for each thread
-  const double* sums = a.sums + ((int64_t)b * a.chunks + tid) * 2;
-  double mine[2] = {0.0, 0.0}, pre[2];
-  if (tid < a.chunks) mine[0] = sums[0], mine[1] = sums[1];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    pre[i] = before(mine[i], waves, tid);
-    if (tid == kWide - 1) total[i] = pre[i] + mine[i];
-  }
-  __syncthreads();
-  const int k = total[0] > 0.0 ? 0 : 1;  // nothing left: the target's row
-  if (!(total[k] > 0.0)) {
-    if (tid == 0) a.next[b] = -1;
-    return;
-  }
-  const float u = a.sample[b];
-  const double share = u < 1.f ? (double)fmaxf(u, 0.f) * total[k] : __builtin_nan("");  // (no sum passes a NaN)
-  if (pre[k] + mine[k] > share && mine[k] > 0.0) atomicMin(&found, tid);
-  if (mine[k] > 0.0) atomicMax(&last, tid);
-  __syncthreads();
-  const int chunk = found < a.chunks ? found : last;  // none passes the share (a random number of 1, or NaN): the last
-  if (tid == chunk) base_of = pre[k];
-  __syncthreads();
-  double base = base_of;
-
-  // the token
-  const int lo = chunk * a.chunk, hi = min(lo + a.chunk, a.V);
+  const float random = a.sample[b];
+  const int64_t at_t = (int64_t)s.row * a.t_row, at_d = (int64_t)s.row * a.d_row;
+  double* sums = a.sums + (int64_t)b * a.units;
   Left l;
   l.scale = scale;
   l.list = list;
-  l.refused = k == 0 ? s.refused : 0;
-  if (!DRAFT && k == 0) pick_listed(a.refused + r.q0, s.refused, lo, hi, list, &listed, tid, kWide);
-  __syncthreads();
-  l.listed = listed;
-  if (tid == 0) {
-    found = a.V;
-    last = -1;
+  l.refused = s.refused;
+  if (DRAFT && a.parents)
+    for (int i = tid; i < s.refused - 1; i += kThreads) scale[i] = a.scales[r.q0 + i];
+
+  // the units' sums, kPer in a row for each thread
+  double mine[kPer], before, total;
+  for (int again = 0;; again = 1) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      mine[i] = kPer * tid + i < a.units ? sums[kPer * tid + i] : 0.0;
+      sum += mine[i];
+    }
+    const double upto = wave_upto(sum);
+    if (lane == 63) waves[wave] = upto;
+    if (tid == 0) {
+      listed = 0;
+      found = a.units;
+      last = -1;
+    }
+    __syncthreads();
+    before = lane_before(upto);
+    total = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) before += waves[w];
+      total += waves[w];
+    }
+    if (total > 0.0 || again) break;
+    // nothing left: the target's row
+    l.refused = 0;
+    for (int u = wave; u < a.units; u += kThreads / 64) {
+      const double x = unit_sum<KIND, DRAFT>(a, at_t, at_d, l, u, lane);
+      if (lane == 63) sums[u] = x;
+    }
+    __syncthreads();  // (the workgroup's own writes, in memory that it alone uses)
   }
+  if (!(total > 0.0)) {
+    if (tid == 0) a.next[b] = -1;
+    return;
+  }
+  const double share = random < 1.f ? (double)fmaxf(random, 0.f) * total : __builtin_nan("");  // (no sum passes a NaN)
+  double upto = before;
+  int first = a.units, top = -1;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    upto += mine[i];
+    if (mine[i] > 0.0) {
+      top = kPer * tid + i;
+      if (first == a.units && upto > share) first = top;
+    }
+  }
+  if (first < a.units) atomicMin(&found, first);
+  if (top >= 0) atomicMax(&last, top);
   __syncthreads();
-  const int64_t at_t = (int64_t)s.row * a.t_row, at_d = (int64_t)s.row * a.d_row;
+  const int unit = found < a.units ? found : last;  // none passes the share (a random number of 1, or NaN): the last
+  if (tid == unit / kPer) {
+    for (int i = 0; i < kPer; ++i)
+      if (i < unit % kPer) before += mine[i];
+    base_of = before;
+  }
+  const int lo = unit * a.unit, hi = (int)min((int64_t)lo + a.unit, (int64_t)a.V);
+  if (!DRAFT) pick_listed(a.refused + r.q0, l.refused, lo, hi, list, &listed, tid, kThreads);
+  __syncthreads();
+  if (wave != 0) return;
+
+  // the token
+  l.listed = uniform(listed);
   const bool draft = DRAFT && l.refused > 0;
-  for (int v0 = lo; v0 < hi; v0 += 8 * kWide) {
-    const int v = v0 + 8 * tid;
+  double base = base_of;
+  int token = -1;
+  for (int v0 = lo; v0 < hi; v0 += kVerifyStep) {
+    const int v = v0 + 8 * lane;
     float pf[8], qf[8];
     double x[8], sum = 0.0;
     load8<KIND>(a.target, at_t, v, hi, pf);
@@ -434,44 +457,45 @@ __global__ __launch_bounds__(kWide) void verify_pick_kernel(const VerifyArgs a) 
     left8(pf, qf, draft, l, v, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += x[i];
-    const double pre = base + before(sum, waves, tid);
-    double upto = pre;
-    int mine = a.V, top = -1;
+    const double all = wave_upto(sum);
+    double now = base + lane_before(all);
+    int here = -1;  // the first that passes the share, or the last that is above 0
+    bool past = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      upto += x[i];
-      if (x[i] > 0.0) {
-        top = v + i;
-        if (mine == a.V && upto > share) mine = v + i;
+      now += x[i];
+      if (x[i] > 0.0 && !past) {
+        here = v + i;
+        past = now > share;
       }
     }
-    if (mine < a.V) atomicMin(&found, mine);
-    if (top >= 0) atomicMax(&last, top);
-    __syncthreads();
-    if (tid == kWide - 1) base_of = pre + sum;
-    __syncthreads();
-    base = base_of;
-    if (found < a.V) break;
+    const uint64_t hit = __ballot(past), some = __ballot(here >= 0);
+    if (hit) {
+      token = __builtin_amdgcn_readlane(here, __builtin_ctzll(hit));
+      break;
+    }
+    if (some) token = __builtin_amdgcn_readlane(here, 63 - __builtin_clzll(some));
+    base += lane_of(all, 63);
   }
-  if (tid == 0) a.next[b] = found < a.V ? found : last;
+  if (lane == 0) a.next[b] = token;
 }
 
 template <int KIND, bool DRAFT>
-hipError_t launch(const VerifyArgs& a, int64_t B, hipStream_t stream) {
-  const dim3 grid((unsigned)a.chunks, (unsigned)B);
+hipError_t launch(const VerifyArgs& a, int64_t B, int64_t chunks, hipStream_t stream) {
+  const dim3 grid((unsigned)chunks, (unsigned)B);
   if (DRAFT && a.parents) {
     hipLaunchKernelGGL((verify_walk_kernel<KIND>), dim3((unsigned)B), dim3(kWide), 0, stream, a);
     hipLaunchKernelGGL((verify_sums_kernel<KIND, DRAFT, DRAFT>), grid, dim3(kThreads), 0, stream, a);
   } else {
     hipLaunchKernelGGL((verify_sums_kernel<KIND, DRAFT, false>), grid, dim3(kThreads), 0, stream, a);
   }
-  hipLaunchKernelGGL((verify_pick_kernel<KIND, DRAFT>), dim3((unsigned)B), dim3(kWide), 0, stream, a);
+  hipLaunchKernelGGL((verify_pick_kernel<KIND, DRAFT>), dim3((unsigned)B), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <int KIND>
-hipError_t launch(const VerifyArgs& a, int64_t B, hipStream_t stream) {
-  return a.draft ? launch<KIND, true>(a, B, stream) : launch<KIND, false>(a, B, stream);
+hipError_t launch(const VerifyArgs& a, int64_t B, int64_t chunks, hipStream_t stream) {
+  return a.draft ? launch<KIND, true>(a, B, chunks, stream) : launch<KIND, false>(a, B, chunks, stream);
 }
 
 }  // namespace
@@ -486,11 +510,11 @@ hipError_t launch_verify(const VerifyProblem& p, const VerifyPlan& pl, void* wor
   a.scales = (double*)(ws + pl.refused);
   a.refused = (int32_t*)(ws + pl.refused);
   a.t_row = p.t_row; a.d_row = p.d_row; a.N = (int32_t)p.N; a.V = (int32_t)p.V; a.depth = (int32_t)p.depth;
-  a.chunk = (int32_t)pl.chunk; a.chunks = (int32_t)pl.chunks;
+  a.unit = (int32_t)pl.unit; a.units = (int32_t)pl.units; a.chunk = (int32_t)pl.chunk;
   switch (p.dtype) {
-    case WQ_F32: return launch<kF32>(a, p.B, stream);
-    case WQ_F16: return launch<kF16>(a, p.B, stream);
-    default: return launch<kBf16>(a, p.B, stream);
+    case WQ_F32: return launch<kF32>(a, p.B, pl.chunks, stream);
+    case WQ_F16: return launch<kF16>(a, p.B, pl.chunks, stream);
+    default: return launch<kBf16>(a, p.B, pl.chunks, stream);
   }
 }
 
