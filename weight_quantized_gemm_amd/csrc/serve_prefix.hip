@@ -149,11 +149,35 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(const JoinArgs a) {
   }
 }
 
+// Prefix and own keys by one launch, where both take the kernel whose waves split the keys (tiles of 16 RT rows): neither
+// waits for the other.
+template <int HD, bool BF16, int RT>
+hipError_t launch_keys(const JoinArgs& a, hipStream_t stream) {
+  using L = KeysLds<HD, RT, true>;
+  const auto kern = tree_keys_kernel<HD, BF16, RT, BothArgs>;
+  const hipError_t e = raise_lds_limit((const void*)kern, L::Total);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(a.shared.blocks + a.own.blocks)), dim3(64 * L::NW), L::Total, stream,
+                     BothArgs{{a.shared, a.own}});
+  return hipGetLastError();
+}
+
 template <int HD, bool BF16>
-hipError_t launch(const JoinArgs& a, const PrefixPlan& pl, hipStream_t stream) {
+hipError_t launch_both(const JoinArgs& a, const PrefixPlan& pl, hipStream_t stream) {
+  if (a.group_count > 0 && !pl.shared.split_rows && !pl.own.split_rows) {
+    if (pl.shared.rows != pl.own.rows) return hipErrorInvalidValue;
+    if constexpr (HD != 256)
+      if (pl.own.rows == 32) return launch_keys<HD, BF16, 2>(a, stream);
+    return launch_keys<HD, BF16, 1>(a, stream);
+  }
   hipError_t e = hipSuccess;
   if (a.group_count > 0) e = launch_parts<HD, BF16>(a.shared, pl.shared, stream);
-  if (e == hipSuccess) e = launch_parts<HD, BF16>(a.own, pl.own, stream);
+  return e == hipSuccess ? launch_parts<HD, BF16>(a.own, pl.own, stream) : e;
+}
+
+template <int HD, bool BF16>
+hipError_t launch(const JoinArgs& a, const PrefixPlan& pl, hipStream_t stream) {
+  const hipError_t e = launch_both<HD, BF16>(a, pl, stream);
   if (e != hipSuccess) return e;
   // the rows' parts are shared by waves where there are four or more of a tile (serve_tree.hip has figures)
   const bool split = pl.own.blocks >= 4 * pl.own.tiles || pl.shared.blocks >= 4 * pl.shared.tiles;

@@ -23,6 +23,7 @@ constexpr int kTreeCutBytes = 32;      // what is noted of a tile for the join
 constexpr int tree_row_keys(int waves) { return waves == 2 ? 32 : 64; }  // keys of a tile whose rows the waves split
 
 // ---- shared prefixes
+constexpr int part_key_waves(int d) { return d == 128 ? 2 : tree_key_waves(d); }
 constexpr int kPrefixGroupBytes = 16;  // what is noted of a group for the join
 
 // ---- verification

@@ -54,6 +54,33 @@ struct PartArgs : TreeArgs {
   int32_t seqs;                 // sequences that group_starts counts in
 };
 
+// Two parts whose workgroups stand one after the other in a launch.
+struct BothArgs {
+  static constexpr bool kParts = true;
+  PartArgs part[2];
+};
+
+// The arguments of a workgroup, and its number in their part.
+__device__ __forceinline__ const TreeArgs& choose(const TreeArgs& a, int&) { return a; }
+__device__ __forceinline__ const PartArgs& choose(const PartArgs& a, int&) { return a; }
+// Read where the kernel's arguments stand: chosen among them by number, they would be copied to scratch memory.
+__device__ __forceinline__ PartArgs choose(const BothArgs&, int& block) {
+  static_assert(sizeof(PartArgs) % 4 == 0 && sizeof(BothArgs) == 2 * sizeof(PartArgs), "whole words");
+  constexpr int kWords = sizeof(PartArgs) / 4;
+  const auto* words = (const __attribute__((address_space(4))) uint32_t*)__builtin_amdgcn_kernarg_segment_ptr();
+  PartArgs a;
+  uint32_t mine[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) mine[i] = words[i];
+  __builtin_memcpy(&a, mine, sizeof(PartArgs));
+  const int own = block >= a.blocks;
+  if (own) block -= a.blocks;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) mine[i] = words[own * kWords + i];
+  __builtin_memcpy(&a, mine, sizeof(PartArgs));
+  return a;
+}
+
 // A base stands kLow below the maximum that sets it, and a weight may pass that maximum's by 2^kSlack.  bf16 has the
 // range of fp32; of fp16's, all of the upper end is used: a weight's last place is 2^-24, so that one loses at
 // most 2^-32 of the largest there (2^-25 with a base at the maximum, which summed up over a long context).
@@ -544,15 +571,23 @@ __device__ __forceinline__ Piece next_piece(const A& a, int lane, int64_t& u, in
 // last tile; returns whether a key is on no page.
 __device__ __forceinline__ int find_slots(const TreeArgs& a, int b, int key0, int count, int* slots, int tid, int threads) {
   int lost = 0;
-  for (int i = tid; i < (count + 63) / 64 * 64; i += threads) {
-    int slot = -1;
-    if (i < count) {
-      const uint32_t key = (uint32_t)(key0 + i), page = divide(key, a.by_page);
-      const int e = a.table[(int64_t)b * a.width + page];
-      if (e >= 0 && e < a.pages) slot = (int)((uint32_t)e * a.by_page.d + (key - page * a.by_page.d));
-      else lost = 1;
+  const int n = (count + 63) / 64 * 64;
+  for (int i0 = tid; i0 < n; i0 += 4 * threads) {  // four of the table's entries on their way at once
+    int e[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = i0 + x * threads;
+      e[x] = i < count ? a.table[(int64_t)b * a.width + divide((uint32_t)(key0 + i), a.by_page)] : -1;
     }
-    slots[i] = slot;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = i0 + x * threads;
+      if (i >= n) continue;
+      const uint32_t key = (uint32_t)(key0 + i), page = divide(key, a.by_page);
+      const bool on = e[x] >= 0 && e[x] < a.pages;
+      lost |= i < count && !on;
+      slots[i] = on ? (int)((uint32_t)e[x] * a.by_page.d + (key - page * a.by_page.d)) : -1;
+    }
   }
   return lost;
 }
@@ -560,10 +595,11 @@ __device__ __forceinline__ int find_slots(const TreeArgs& a, int b, int key0, in
 // This workgroup's share of all `total` units; false: none.  Shares in a row stand on one XCD
 // (workgroups go round the 8 XCDs), so that tiles of the same keys meet in its L2.
 template <class A>
-__device__ __forceinline__ bool my_share(const A& a, int lane, int64_t& total, int64_t& me, int64_t& u, int64_t& u_end) {
+__device__ __forceinline__ bool my_share(const A& a, int block, int lane, int64_t& total, int64_t& me, int64_t& u,
+                                         int64_t& u_end) {
   total = uniform(total_units(a, lane));
   const int64_t n = shares(a, total);
-  me = blockIdx.x;
+  me = block;
   if (n == 0 && me == 0 && threadIdx.x == 0) *a.tiles = 0;
   if (me >= n) return false;
   if ((n & 7) == 0) me = (me & 7) * (n >> 3) + (me >> 3);
@@ -599,19 +635,21 @@ __device__ __forceinline__ int64_t part_place(const PartArgs& a, int64_t me, con
 }
 
 // ------------------------------------------------------------------------------ waves split the keys
-template <int HD, int RT>
+template <int HD, int RT, bool PARTS>
 struct KeysLds {
-  static constexpr int NW = tree_key_waves(HD), R = 16 * RT, Pad = HD + 4;  // Pad: floats of a joining row
+  static constexpr int NW = PARTS ? part_key_waves(HD) : tree_key_waves(HD), R = 16 * RT, Pad = HD + 4;  // Pad: floats of a joining row
   // the waves' stages, later their rows
   static constexpr int Area = std::max(NW * 2 * Cfg<HD, 32>::Stage, NW * R * Pad * 4);
-  static constexpr int Slots = HD == 64 ? 2048 : 4096;          // keys whose slots stand in LDS at a time
+  static constexpr int Slots = HD == 64 || PARTS ? 2048 : 4096;  // keys whose slots stand in LDS at a time
   static constexpr int Total = Area + Slots * 4 + NW * R * 8;  // slots, (base, sum) of each wave's rows
 };
 
 template <int HD, bool BF16, int RT, class A>
-__global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tree_keys_kernel(const A a) {
+__global__ __launch_bounds__((64 * KeysLds<HD, RT, A::kParts>::NW), HD == 256 ? 1 : 2) void tree_keys_kernel(const A args) {
+  int block = (int)blockIdx.x;
+  const auto& a = choose(args, block);
   using C = Cfg<HD, 32>;
-  using L = KeysLds<HD, RT>;
+  using L = KeysLds<HD, RT, A::kParts>;
   constexpr int R = L::R, NW = L::NW;
   extern __shared__ __align__(16) uint8_t lds[];
   int* slots = (int*)(lds + L::Area);
@@ -619,7 +657,7 @@ __global__ __launch_bounds__(64 * tree_key_waves(HD), HD == 256 ? 1 : 2) void tr
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int64_t total, me, u, u_end;
-  if (!my_share(a, lane, total, me, u, u_end)) return;
+  if (!my_share(a, block, lane, total, me, u, u_end)) return;
 
   while (u < u_end) {
     const Piece p = next_piece(a, lane, u, u_end);
@@ -753,7 +791,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tree_rows_kernel(const A a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int64_t total, me, u, u_end;
-  if (!my_share(a, lane, total, me, u, u_end)) return;
+  if (!my_share(a, (int)blockIdx.x, lane, total, me, u, u_end)) return;
 
   while (u < u_end) {
     const Piece p = next_piece(a, lane, u, u_end);
@@ -838,10 +876,10 @@ hipError_t launch_parts(const A& a, const TreePlan& pl, hipStream_t stream) {
   const void* kern = nullptr;
   int threads = 64 * pl.waves, lds = 0;
   if (!pl.split_rows) {
-    threads = 64 * tree_key_waves(HD);
-    if (pl.rows == 16) kern = (const void*)tree_keys_kernel<HD, BF16, 1, A>, lds = KeysLds<HD, 1>::Total;
+    threads = 64 * KeysLds<HD, 1, A::kParts>::NW;
+    if (pl.rows == 16) kern = (const void*)tree_keys_kernel<HD, BF16, 1, A>, lds = KeysLds<HD, 1, A::kParts>::Total;
     if constexpr (HD != 256)
-      if (pl.rows == 32) kern = (const void*)tree_keys_kernel<HD, BF16, 2, A>, lds = KeysLds<HD, 2>::Total;
+      if (pl.rows == 32) kern = (const void*)tree_keys_kernel<HD, BF16, 2, A>, lds = KeysLds<HD, 2, A::kParts>::Total;
   } else if constexpr (HD != 256) {
     if (pl.waves == 2) kern = (const void*)tree_rows_kernel<HD, BF16, 2, A>, lds = RowsLds<HD, 2>::Total;
     if (pl.waves == 4) kern = (const void*)tree_rows_kernel<HD, BF16, 4, A>, lds = RowsLds<HD, 4>::Total;
