@@ -10,7 +10,6 @@
 // second piece is any other.  Where the halves are not whole pieces, a lane finds the partners of its
 // elements in LDS.  A head of v, and elements past the rotated part, are copied.
 //
-// A lane takes the same head of kTokens tokens in a row: what it is, its weights and its strides are found once.
 // The workgroup computes the cosines and sines of its tokens once, in LDS, for all heads; angles are products in fp64,
 // taken in turns and reduced to half a turn before they become fp32.
 #include <algorithm>
@@ -22,7 +21,6 @@ namespace wq {
 namespace {
 
 constexpr double kInvTwoPi = 0.15915494309189533577;
-constexpr int kTokens = 2;
 enum Mode { kHalf, kPairs, kOdd };  // half layout in whole 8s; interleaved; half layout otherwise
 
 struct NormRopeArgs {
@@ -34,7 +32,9 @@ struct NormRopeArgs {
   int32_t wide[3];                        // weights in fp32
   const int32_t *positions, *slots, *axis_of;
   const float* inv_freq;
-  int64_t T, S, block0;
+  int64_t T, S;
+  int64_t t_base;                         // the launch's first token, and the first of its heads
+  int32_t h_base;
   int32_t hq, hkv, heads, half, d, axes;  // heads: of a token, v's among them
   int32_t turn_units, units, second;      // lanes of a head whose pieces turn (kHalf), all of them; pieces to the second
   FastDiv by_heads, by_half;
@@ -87,19 +87,18 @@ template <bool BF16, int G, int MODE>
 __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a) {
   extern __shared__ __align__(16) float2 turns[];  // (cos, sin) of each token of the workgroup and each pair
   __shared__ __align__(16) float rows[MODE == kOdd ? 256 * 16 : 1];
-  constexpr int Groups = 256 / G, E = kTokens;
+  constexpr int Groups = 256 / G;
   const int tid = threadIdx.x, unit = tid % G, group = tid / G;
-  // heads of E tokens each, one for a group of lanes
-  const int64_t first = (a.block0 + blockIdx.x) * Groups, blocks_of_t = (a.T + E - 1) / E, last = blocks_of_t * a.heads;
-  const int64_t t0 = first / a.heads * E;
-  const int h0 = (int)(first - t0 / E * a.heads);
+  // one head for a group of lanes; a launch has fewer than 2^30
+  const uint32_t first = (uint32_t)a.h_base + blockIdx.x * Groups, before = divide(first, a.by_heads);
+  const int64_t t0 = a.t_base + before;
+  const int h0 = (int)(first - before * (uint32_t)a.heads);
   const uint32_t left = (uint32_t)min(a.T - t0, (int64_t)1 << 20);  // tokens from t0 on
-  const int tokens = (int)min((int64_t)left, ((min(first + Groups, last) - 1) / a.heads + 1) * E - t0);
+  const int tokens = (int)min(left, divide((uint32_t)(h0 + Groups - 1), a.by_heads) + 1);
 
-  // this lane's head, its first token of the workgroup, and its pieces
-  const uint32_t x0 = (uint32_t)(h0 + group), tb = divide(x0, a.by_heads);
-  const int head = (int)(x0 - tb * (uint32_t)a.heads);
-  const uint32_t token = tb * E;
+  // this lane's head, its token of the workgroup's, and its pieces
+  const uint32_t x0 = (uint32_t)(h0 + group), token = divide(x0, a.by_heads);
+  const int head = (int)(x0 - token * (uint32_t)a.heads);
   const int kind = head < a.hq ? 0 : head < a.hq + a.hkv ? 1 : 2;
   const int h = head - (kind == 0 ? 0 : kind == 1 ? a.hq : a.hq + a.hkv);
   const bool turning = MODE != kHalf || unit < a.turn_units;
@@ -111,21 +110,15 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a) {
 
   const int64_t src_t = pick(a.src_t, kind);
   const uint16_t* src = pick(a.src, kind) + t0 * src_t + (uint64_t)token * src_t + (uint64_t)(uint32_t)h * pick(a.src_h, kind);
-  uint16_t* dst[E];
-  u32x4_t x[E], y[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    x[e] = y[e] = u32x4_t{0, 0, 0, 0};
-    dst[e] = nullptr;
-    if (!one || token + e >= left) continue;
-    x[e] = *(const u32x4_t*)(src + e * src_t + lo);
-    if (two) y[e] = *(const u32x4_t*)(src + e * src_t + hi);
-    int64_t row = t0 + token + e;
-    if (kind != 0) {
-      if (a.slots) row = a.slots[row];
-      if (row < 0 || row >= a.S) continue;  // no token's row: its k and v are dropped
-    }
-    dst[e] = pick(a.dst, kind) + row * pick(a.dst_t, kind) + (uint64_t)(uint32_t)h * pick(a.dst_h, kind);
+  uint16_t* dst = nullptr;  // null: no token, or one whose slot drops its k and v
+  u32x4_t x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+  if (one) {
+    x = *(const u32x4_t*)(src + lo);
+    if (two) y = *(const u32x4_t*)(src + hi);
+    int64_t row = t0 + token;
+    if (kind != 0 && a.slots) row = a.slots[row];
+    if (kind == 0 || (row >= 0 && row < a.S))
+      dst = pick(a.dst, kind) + row * pick(a.dst_t, kind) + (uint64_t)(uint32_t)h * pick(a.dst_h, kind);
   }
   float wl[8], wh[8];
   if (weight && one) {
@@ -144,92 +137,87 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a) {
   }
   __syncthreads();
 
+  float f[8], g[8];
+  widen<BF16>(x, f);
+  widen<BF16>(y, g);
+  if (weight) {
+    float sum = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    float f[8], g[8];
-    widen<BF16>(x[e], f);
-    widen<BF16>(y[e], g);
-    if (weight) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], fmaf(g[i], g[i], sum));
-      sum = group_sum<G>(sum);
-      float by = __builtin_amdgcn_rsqf(fmaf(sum, a.inv_d, a.eps));
-      if (BF16 && !(sum < __builtin_inff())) {  // squares of bf16 pass fp32: with a factor of 2^-70
-        constexpr float kDown = 0x1p-70f;
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] *= kDown;
-          g[i] *= kDown;
-          sum = fmaf(f[i], f[i], fmaf(g[i], g[i], sum));
-        }
-        by = __builtin_amdgcn_rsqf(group_sum<G>(sum) * a.inv_d);
-      }
-      if (one)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] *= by * wl[i];
-          if (two) g[i] *= by * wh[i];
-        }
-    }
-    const float2* cs = turns + (token + e) * a.half;
-    if constexpr (MODE == kOdd) {
-      float* row = rows + 16 * G * group;
-      if (kind < 2 && one) {
-        *(f32x4_t*)(row + lo) = f32x4_t{f[0], f[1], f[2], f[3]};
-        *(f32x4_t*)(row + lo + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
-        if (two) {
-          *(f32x4_t*)(row + hi) = f32x4_t{g[0], g[1], g[2], g[3]};
-          *(f32x4_t*)(row + hi + 4) = f32x4_t{g[4], g[5], g[6], g[7]};
-        }
-      }
-      // the group's lanes are of one wave: what they wrote is there once its LDS writes are done
-      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
-      __builtin_amdgcn_wave_barrier();
-      auto turned = [&](float mine, int at) {
-        if (at >= 2 * a.half) return mine;
-        const bool low = at < a.half;
-        const float other = row[low ? at + a.half : at - a.half];
-        const float2 z = cs[low ? at : at - a.half];
-        return low ? mine * z.x - other * z.y : mine * z.x + other * z.y;
-      };
-      if (kind < 2 && one && dst[e])
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] = turned(f[i], lo + i);
-          if (two) g[i] = turned(g[i], hi + i);
-        }
-      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
-      __builtin_amdgcn_wave_barrier();
-    } else if constexpr (MODE == kPairs) {
-      auto turn = [&](float* v, int at) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          if (at / 2 + p < a.half) {
-            const float2 z = cs[at / 2 + p];
-            const float u = v[2 * p], w = v[2 * p + 1];
-            v[2 * p] = u * z.x - w * z.y;
-            v[2 * p + 1] = w * z.x + u * z.y;
-          }
-      };
-      if (kind < 2 && dst[e]) {
-        turn(f, lo);
-        if (two) turn(g, hi);
-      }
-    } else if (kind < 2 && turning && dst[e]) {
+    for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], fmaf(g[i], g[i], sum));
+    sum = group_sum<G>(sum);
+    float by = __builtin_amdgcn_rsqf(fmaf(sum, a.inv_d, a.eps));
+    if (BF16 && !(sum < __builtin_inff())) {  // squares of bf16 pass fp32: with a factor of 2^-70
+      constexpr float kDown = 0x1p-70f;
+      sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 z = cs[lo + i];
-        const float u = f[i], v = g[i];
-        f[i] = u * z.x - v * z.y;
-        g[i] = v * z.x + u * z.y;
+        f[i] *= kDown;
+        g[i] *= kDown;
+        sum = fmaf(f[i], f[i], fmaf(g[i], g[i], sum));
+      }
+      by = __builtin_amdgcn_rsqf(group_sum<G>(sum) * a.inv_d);
+    }
+    if (one)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] *= by * wl[i];
+        if (two) g[i] *= by * wh[i];
+      }
+  }
+  const float2* cs = turns + token * a.half;
+  if constexpr (MODE == kOdd) {
+    float* row = rows + 16 * G * group;
+    if (kind < 2 && one) {
+      *(f32x4_t*)(row + lo) = f32x4_t{f[0], f[1], f[2], f[3]};
+      *(f32x4_t*)(row + lo + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
+      if (two) {
+        *(f32x4_t*)(row + hi) = f32x4_t{g[0], g[1], g[2], g[3]};
+        *(f32x4_t*)(row + hi + 4) = f32x4_t{g[4], g[5], g[6], g[7]};
       }
     }
-    if (!dst[e]) continue;
-    *(u32x4_t*)(dst[e] + lo) = kind < 2 ? narrow<BF16>(f) : x[e];
-    if (two) *(u32x4_t*)(dst[e] + hi) = kind < 2 ? narrow<BF16>(g) : y[e];
+    // the group's lanes are of one wave: what they wrote is there once its LDS writes are done
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+    __builtin_amdgcn_wave_barrier();
+    auto turned = [&](float mine, int at) {
+      if (at >= 2 * a.half) return mine;
+      const bool low = at < a.half;
+      const float other = row[low ? at + a.half : at - a.half];
+      const float2 z = cs[low ? at : at - a.half];
+      return low ? mine * z.x - other * z.y : mine * z.x + other * z.y;
+    };
+    if (kind < 2 && one && dst)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = turned(f[i], lo + i);
+        if (two) g[i] = turned(g[i], hi + i);
+      }
+  } else if constexpr (MODE == kPairs) {
+    auto turn = [&](float* v, int at) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (at / 2 + p < a.half) {
+          const float2 z = cs[at / 2 + p];
+          const float u = v[2 * p], w = v[2 * p + 1];
+          v[2 * p] = u * z.x - w * z.y;
+          v[2 * p + 1] = w * z.x + u * z.y;
+        }
+    };
+    if (kind < 2 && dst) {
+      turn(f, lo);
+      if (two) turn(g, hi);
+    }
+  } else if (kind < 2 && turning && dst) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 z = cs[lo + i];
+      const float u = f[i], v = g[i];
+      f[i] = u * z.x - v * z.y;
+      g[i] = v * z.x + u * z.y;
+    }
   }
+  if (!dst) return;
+  *(u32x4_t*)(dst + lo) = kind < 2 ? narrow<BF16>(f) : x;
+  if (two) *(u32x4_t*)(dst + hi) = kind < 2 ? narrow<BF16>(g) : y;
 }
 
 template <bool BF16, int MODE>
@@ -241,13 +229,15 @@ hipError_t launch(NormRopeArgs a, hipStream_t stream) {
     case 8: kern = norm_rope_kernel<BF16, 8, MODE>; break;
     default: kern = norm_rope_kernel<BF16, 16, MODE>; break;
   }
-  const int64_t groups = 256 / g, blocks = ((a.T + kTokens - 1) / kTokens * a.heads + groups - 1) / groups;
-  // tokens that this many heads in a row can touch: at most 40 KB of LDS
-  const int64_t tokens = std::min<int64_t>(a.T, (groups / a.heads + 2) * kTokens);
+  const int64_t groups = 256 / g, blocks = (a.T * a.heads + groups - 1) / groups;
+  // tokens that this many heads in a row can touch: at most 20 KB of LDS
+  const int64_t tokens = std::min<int64_t>(a.T, groups / a.heads + 2);
   const size_t lds = (size_t)tokens * a.half * sizeof(float2);
   constexpr int64_t kMost = 1 << 23;  // workgroups of one launch: its threads stay below 2^32
-  for (a.block0 = 0; a.block0 < blocks; a.block0 += kMost) {
-    hipLaunchKernelGGL(kern, dim3((unsigned)std::min(kMost, blocks - a.block0)), dim3(256), lds, stream, a);
+  for (int64_t b = 0; b < blocks; b += kMost) {
+    a.t_base = b * groups / a.heads;
+    a.h_base = (int32_t)(b * groups % a.heads);
+    hipLaunchKernelGGL(kern, dim3((unsigned)std::min(kMost, blocks - b)), dim3(256), lds, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
