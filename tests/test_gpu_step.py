@@ -136,6 +136,16 @@ def test_layout_ends_of_the_ranges():
     check_layout([100, 3], [2, 1], [[1], [2]], [], 0, 3, 128, offsets=[2 ** 31 - 101, -50], what="positions")
 
 
+def test_layout_more_tokens_than_passes():
+    """So many tokens that a workgroup takes several passes of them, with parents that are staged anew for each."""
+    say("layout passes")
+    check_layout(**layout_case(21, 200, 3000, 16, tree=False), what="passes")
+    new, n = [1300] * 250, 250 * 1300 + 7
+    parents = [j - 1 if j % 1000 else max(j - 1, 0) - 900 * (j > 0) if j else -1 for _ in new for j in range(1300)] + [0] * 7
+    check_layout([5] * 250, new, [[3] + [-1] * 90] * 250, list(range(25000)), 25000, n, 16, None, parents, 3, what="trees")
+    check_layout(**layout_case(22, 1500, 1500, 16), what="wide passes")
+
+
 def test_layout_trees():
     say("layout trees")
     # parents that are none, deep chains (longer than what stands in LDS), a mask with too few words or none
