@@ -335,6 +335,19 @@ def test_norm_rope_sizes_of_numbers(i):
     assert torch.equal(torch.isnan(out[3, 2]).cpu(), torch.isnan(ref[0, 2])) and torch.isnan(ref[0, 2]).any()
 
 
+@pytest.mark.parametrize("i", [1, 4, 6])
+@pytest.mark.parametrize("far", [18, -18])
+def test_norm_rope_weights_far_from_one(i, far):
+    """Heads of 2^(3 far) under weights (fp32) of 2^(-5 far): the root's inverse times the weight leaves fp32's normal
+    numbers, the result does not."""
+    say("norm_rope far weights", i, far)
+    T, hq, hkv, d, rot, inter = 4, 6, 2, *NORM[i][3:6]
+    c = norm_case(i, torch.bfloat16, T, hq, hkv, d, rot, inter, 1, "32", True)
+    c["q"], c["q_weight"] = c["q"] * 2.0 ** (3 * far), torch.ones(d, device=DEV) * 2.0 ** (-5 * far)
+    c["eps"] = 1e-36
+    norm_check(c, W.norm_rope(**c), "far")
+
+
 def test_norm_rope_large():
     """More heads in a row than one workgroup has, 64-bit offsets, far positions."""
     say("norm_rope large")

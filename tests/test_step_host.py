@@ -66,6 +66,13 @@ def test_norm_rope_accepts_no_tokens(wqlib):
     assert norm(wqlib, k=None, v=None, k_weight=None, slots=None, k_out=None, v_out=None) == OK
 
 
+def test_norm_rope_smallest_eps(wqlib):
+    """eps is fp32's smallest normal number at least: the root of a head of zeros is finite."""
+    args = norm_args(T=5)
+    assert norm(wqlib, **{**args, "eps": 2.0 ** -127}) == INVALID
+    assert norm(wqlib, eps=2.0 ** -126) == OK
+
+
 def test_norm_rope_refuses(wqlib):
     args = norm_args(T=5)
     call = lambda **kw: norm(wqlib, **kw)

@@ -159,9 +159,9 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a) {
     }
     if (one)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] *= by * wl[i];
-        if (two) g[i] *= by * wh[i];
+      for (int i = 0; i < 8; ++i) {  // the norm first: of a head and a weight far from 1, by * weight leaves fp32
+        f[i] = f[i] * by * wl[i];
+        if (two) g[i] = g[i] * by * wh[i];
       }
   }
   const float2* cs = turns + token * a.half;
