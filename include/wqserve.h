@@ -243,6 +243,8 @@ int wq_prefix_attention(const wq_tensor* q, const wq_tensor* k_cache, const wq_t
  * (no such x, for a random number of 1 or NaN: the largest with r[x] > 0); where nothing is left of r, the target's
  * row stands for it, and where that holds nothing above 0, the token is -1.  Probabilities that are negative
  * or NaN count as 0.  What is compared or summed is fp64.
+ * With draft and parents, a refusal that is followed by another child of the same token takes a pass over the
+ * two rows, one after the other within a request.
  *
  *   target         required; WQ_F32, WQ_F16 or WQ_BF16; (N, V): row i, the probabilities after token i; V in
  *                  [1, 2^24], N at most 2^24.  The last axis is contiguous, the row stride at least V.

@@ -68,7 +68,7 @@ struct VerifyProblem {
 struct VerifyPlan {
   int64_t unit = 0, units = 0;    // probabilities of a sum, and sums of a row
   int64_t chunk = 0, chunks = 0;  // units of a workgroup, and workgroups of a row
-  int64_t sums = 0, refused = 0;  // offsets in bytes: the units' sums; the refused tokens or their scales
+  int64_t sums = 0, refused = 0;  // offsets in bytes: the units' sums; the refused tokens (without draft)
   int64_t workspace = 0;          // states first
 };
 constexpr int kVerifyStateBytes = 16;

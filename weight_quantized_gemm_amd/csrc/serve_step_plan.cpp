@@ -57,7 +57,7 @@ VerifyPlan plan_verify(const VerifyProblem& p) {
   pl.chunks = ceil_div(pl.units, pl.chunk);
   pl.sums = align256(p.B * kVerifyStateBytes);
   pl.refused = pl.sums + align256(p.B * pl.units * 8);
-  pl.workspace = pl.refused + align256(p.N * 8);
+  pl.workspace = pl.refused + (p.draft ? 0 : align256(p.N * 4));
   return pl;
 }
 
