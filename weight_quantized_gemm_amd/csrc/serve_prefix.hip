@@ -185,8 +185,7 @@ template <int HD, bool BF16>
 hipError_t launch(const JoinArgs& a, const PrefixPlan& pl, hipStream_t stream) {
   const hipError_t e = launch_both<HD, BF16>(a, pl, stream);
   if (e != hipSuccess) return e;
-  // the rows' parts are shared by waves where there are four or more of a tile (serve_tree.hip has figures)
-  const bool split = pl.own.blocks >= 4 * pl.own.tiles || pl.shared.blocks >= 4 * pl.shared.tiles;
+  const bool split = pl.split_join;
   const int rows = split ? prefix_join_rows<HD, true>() : prefix_join_rows<HD, false>();
   const dim3 grid((unsigned)std::min<int64_t>(pl.own.tiles, 1 << 20), (unsigned)((pl.own.rows + rows - 1) / rows));
   if (split) hipLaunchKernelGGL((prefix_join_kernel<HD, BF16, true>), grid, dim3(256), 0, stream, a);

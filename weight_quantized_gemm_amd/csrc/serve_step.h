@@ -44,6 +44,7 @@ struct PrefixProblem {
 
 struct PrefixPlan {
   TreePlan own, shared;
+  bool split_join = false;  // whether four waves share the parts of a row
   // offsets in bytes; parts: two of each workgroup, then one for each tile
   int64_t shared_notes = 0, own_notes = 0, groups = 0, shared_parts = 0, own_parts = 0;
   int64_t workspace = 0;

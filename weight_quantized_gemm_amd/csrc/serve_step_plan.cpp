@@ -34,6 +34,9 @@ PrefixPlan plan_prefix(const PrefixProblem& p) {
   };
   fit(pl.own, p.own);
   fit(pl.shared, p.shared);
+  // Where a tile of either kind has four parts or more (serve_tree.hip's join has figures of both sides).
+  auto many = [](const TreePlan& t) { return t.tiles > 0 && t.blocks >= 4 * t.tiles; };
+  pl.split_join = many(pl.own) || many(pl.shared);
   int64_t at = 0;
   auto take = [&](int64_t bytes) { const int64_t here = at; at += align256(bytes); return here; };
   auto parts = [&](const TreePlan& t) { return (2 * t.blocks + t.tiles) * t.rows * (int64_t)(p.own.d + 2) * 4; };
