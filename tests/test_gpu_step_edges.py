@@ -1,13 +1,51 @@
-"""Further cases of the serving operators around a step's attention (GPU): many refused drafts, and bounds that are narrower
-than those of test_gpu_step.py."""
+"""Further cases of the serving operators around a step's attention (GPU): many refused drafts, and tables made by hand."""
 import pytest
 import torch
 
 import weight_quantized_gemm_amd as W
-from test_gpu_serve import DEV, gen, say
-from test_gpu_step import ints, verify_case, verify_check
+from test_gpu_serve import DEV, DTYPES, gen, rnd, say
+from test_gpu_step import ints, layout_ref, verify_case, verify_check
 
 pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------------------------- layout
+
+@pytest.mark.parametrize("dt", DTYPES, ids=["bf16", "fp16"])
+def test_layout_feeds_rope_and_attention(dt):
+    """rope and tree_attention over the layout's tables give, bit for bit, what they give over tables made by hand, in the
+    cache's rows too."""
+    say("layout by hand", dt)
+    page, ctx, new, rest = 16, [37, 0, 128, 15, 31], [5, 3, 1, 9, 2], 4
+    g = gen(740)
+    parents = [int(torch.randint(-1, j, (1,), generator=g)) if j else -1 for t in new for j in range(t)] + [0] * rest
+    have = [-(-x // page) for x in ctx]
+    ids = torch.randperm(sum(have) + 9, generator=g).tolist()
+    table, at = [], 0
+    for h in have:
+        table.append((ids[at:at + h] + [-1] * 10)[:10])
+        at += h
+    n, free = sum(new) + rest, ids[at:]
+    hand = layout_ref(ctx, new, table, free, n, page, [7] * 5, parents, 1)
+    given = ints(table)
+    out = W.step_layout(ints(ctx), ints(new), given, ints(free), ints([len(free)]), tokens=n, page_size=page,
+                        position_offsets=ints([7] * 5), parents=ints(parents), mask_words=1)
+    q, k, v = (rnd(g, n, h, 64, dtype=dt) for h in (4, 2, 2))
+    caches = [rnd(g, len(ids) * page, 2, 64, dtype=dt) for _ in range(2)]
+    freq = W.rope_frequencies(64, device=DEV)[0]
+
+    def step(positions, slots, table, starts, mask):
+        kc, vc = (c.clone() for c in caches)
+        turned = W.rope(q, k, v, positions, freq, slots=slots, k_out=kc, v_out=vc)[0]
+        o = torch.zeros_like(q)
+        W.tree_attention(turned, kc, vc, table, ints(ctx), starts, mask, page_size=page, out=o)
+        return turned, kc, vc, o
+
+    want = step(ints(hand["positions"]), ints(hand["slots"]), ints(hand["table"]), ints(hand["q_starts"]), ints(hand["tree_mask"]))
+    got = step(out.positions, out.slots, given, out.q_starts, out.tree_mask)
+    for name, a, b in zip(("q", "k cache", "v cache", "output"), got, want):
+        assert torch.equal(a, b), name
+    assert not torch.equal(want[1], caches[0]) and want[3][:sum(new)].any(dim=-1).all() and not want[3][sum(new):].any()
 
 
 # --------------------------------------------------------------------------------------------- verify
