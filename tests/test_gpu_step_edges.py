@@ -1,10 +1,11 @@
-"""Further cases of the serving operators around a step's attention (GPU): many refused drafts, and tables made by hand."""
+"""Further cases of the serving operators around a step's attention (GPU): many refused drafts, tables made by hand, and a
+bound of prefix attention that is narrower than test_gpu_step.py's."""
 import pytest
 import torch
 
 import weight_quantized_gemm_amd as W
-from test_gpu_serve import DEV, DTYPES, gen, rnd, say
-from test_gpu_step import ints, layout_ref, verify_case, verify_check
+from test_gpu_serve import DEV, DTYPES, E, SUB, U, close, gen, rnd, say
+from test_gpu_step import ints, layout_ref, prefix_case, prefix_run, verify_case, verify_check
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +47,66 @@ def test_layout_feeds_rope_and_attention(dt):
     for name, a, b in zip(("q", "k cache", "v cache", "output"), got, want):
         assert torch.equal(a, b), name
     assert not torch.equal(want[1], caches[0]) and want[3][:sum(new)].any(dim=-1).all() and not want[3][sum(new):].any()
+
+
+# --------------------------------------------------------------------------------------------- prefix
+
+def narrow_ref(c, dt):
+    """(result, bound, result of weights rounded to one 16-bit term) of tokens that see the whole prefix and their own
+    sequence's keys up to themselves.
+
+    u = U: the result's rounding, u |out|.  A weight enters both sums as two 16-bit terms, off by u^2 of it (and in fp16, where the
+    second term may be subnormal, by 2^-32 of the largest), in the sum of products and in the sum below it: 2 u^2 mag,
+    mag = sum p |v|, and 2^-31 of the largest weight times sum |v|.  Scores of d products in fp32, ds = 2 (d + 4) e scale
+    |q| |k| with e = 2^-24, move each weight and the sum: 4 ds mag.  The exponent's argument (below 8: scores here are
+    below 1, and fp16's base is 7 lower) and exp2 itself: 10 e a weight, 20 e mag.  2 n products to a sum, both sums: 4 n e mag;
+    joining waves and parts: 20 e mag.  One 16-bit term would be off by up to u of each weight."""
+    q, k, v = (c[x].double().cpu() for x in ("q", "k", "v"))
+    ptable, table, page, starts = c["ptable"].cpu().long(), c["table"].cpu().long(), c["page"], c["starts"].tolist()
+    n, hq, d = q.shape
+    hkv, u, low = k.shape[1], U[dt], 0 if dt == torch.bfloat16 else 7
+    out, bound, one = (torch.zeros_like(q) for _ in range(3))
+    for b, (ctx, t) in enumerate(c["seqs"]):
+        g = [i for i in range(len(c["prefixes"])) if c["first"][i] <= b < c["first"][i + 1]][0]
+        j = torch.arange(c["prefixes"][g][0])
+        shared = ptable[g, j // page] * page + j % page
+        for i in range(t):
+            j = torch.arange(ctx + i + 1)
+            rows = torch.cat((shared, table[b, j // page] * page + j % page))
+            for h in range(hkv):
+                mine = slice(h * hq // hkv, (h + 1) * hq // hkv)
+                x, kk, vv = q[starts[b] + i, mine], k[rows, h], v[rows, h]
+                s = d ** -0.5 * x @ kk.t()
+                p = s.softmax(-1)
+                assert (s.amax(-1) - s.amin(-1)).max() < 1
+                out[starts[b] + i, mine] = p @ vv
+                mag = p @ vv.abs()
+                ds = (2 * (d + 4) * E * d ** -0.5 * (x.abs() @ kk.abs().t())).amax(-1, keepdim=True)
+                sub = 2.0 ** -31 * p.amax(-1, keepdim=True) * vv.abs().sum(0) if low else 0.0
+                bound[starts[b] + i, mine] = (u * out[starts[b] + i, mine].abs() + SUB[dt] + sub
+                                              + (2 * u * u + 4 * ds + (4 * len(rows) + 40) * E) * mag)
+                w = (2.0 ** low * (s - s.amax(-1, keepdim=True)).exp()).to(dt).double()
+                one[starts[b] + i, mine] = w @ vv / w.sum(-1, keepdim=True)
+    return out, bound, one
+
+
+@pytest.mark.parametrize("dt", DTYPES, ids=["bf16", "fp16"])
+@pytest.mark.parametrize("prefixes,seqs,hq,hkv,d", [
+    ([(9, 2), (11, 2)], [(3, 1), (0, 2), (7, 1), (2, 2)], 8, 2, 64),    # waves that split the keys
+    ([(13, 4)], [(3, 1), (0, 2), (7, 1), (2, 2)], 8, 2, 128),
+    ([(6, 8)], [(1 + i, 2) for i in range(8)], 8, 4, 256),
+    ([(12, 16)], [(i % 5, 2) for i in range(16)], 8, 1, 128),           # waves that split the rows: 256 of them
+    ([(10, 9)], [(i % 5, 3) for i in range(9)], 8, 2, 64),              # 108
+    ([(10, 4)], [(3, 17)] * 4, 8, 2, 128),                              # and the own keys' 68
+], ids=str)
+def test_prefix_weights_have_two_terms(prefixes, seqs, hq, hkv, d, dt):
+    """Few keys of nearly equal weights: where values cancel, one 16-bit term a weight would show, as it does in the
+    plain computation with weights rounded once."""
+    say("prefix narrow", prefixes, hq, hkv, d, dt)
+    c = prefix_case(750, dt, prefixes, seqs, hq, hkv, d, 16, std=2.0 ** -6)
+    ref, bound, one = narrow_ref(c, dt)
+    assert ((one - ref).abs() > bound).any()
+    close(prefix_run(c), ref, bound, (prefixes, d))
 
 
 # --------------------------------------------------------------------------------------------- verify
