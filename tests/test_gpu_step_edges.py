@@ -1,11 +1,12 @@
-"""Further cases of the serving operators around a step's attention (GPU): many refused drafts, tables made by hand, and a
-bound of prefix attention that is narrower than test_gpu_step.py's."""
+"""Further cases of the serving operators around a step's attention (GPU): many refused drafts, tables made by hand, large
+eps, and a bound of prefix attention that is narrower than test_gpu_step.py's."""
 import pytest
 import torch
 
 import weight_quantized_gemm_amd as W
 from test_gpu_serve import DEV, DTYPES, E, SUB, U, close, gen, rnd, say
-from test_gpu_step import ints, layout_ref, prefix_case, prefix_run, verify_case, verify_check
+from test_gpu_step import (NORM, ints, layout_ref, norm_case, norm_check, prefix_case, prefix_run, verify_case,
+                           verify_check)
 
 pytestmark = pytest.mark.gpu
 
@@ -47,6 +48,21 @@ def test_layout_feeds_rope_and_attention(dt):
     for name, a, b in zip(("q", "k cache", "v cache", "output"), got, want):
         assert torch.equal(a, b), name
     assert not torch.equal(want[1], caches[0]) and want[3][:sum(new)].any(dim=-1).all() and not want[3][sum(new):].any()
+
+
+# ------------------------------------------------------------------------------------------ norm_rope
+
+@pytest.mark.parametrize("i", [1, 4, 6, 8, 9])
+@pytest.mark.parametrize("size,eps", [(64, 2.0 ** 126), (66, 2.0 ** 127), (61, 2.0 ** 128 - 2.0 ** 104), (63, 2.0 ** 126),
+                                      (64, 1e-6), (0, 2.0 ** 126), (-63, 2.0 ** -126), (-66, 2.0 ** -126)])
+def test_norm_rope_eps_beside_large_heads(i, size, eps):
+    """Heads (bf16) whose squares, or their mean with eps, leave fp32 upwards, or its normal numbers downwards: eps is as
+    large as they are."""
+    say("norm_rope eps", i, size, eps)
+    T, hq, hkv, d, rot, inter = 4, 6, 2, *NORM[i][3:6]
+    c = norm_case(i, torch.bfloat16, T, hq, hkv, d, rot, inter, 1, "16", True)
+    c["q"], c["eps"] = c["q"] * 2.0 ** size, eps
+    norm_check(c, W.norm_rope(**c), (i, size, eps))
 
 
 # --------------------------------------------------------------------------------------------- prefix

@@ -148,8 +148,9 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], fmaf(g[i], g[i], sum));
     sum = group_sum<G>(sum);
-    float by = __builtin_amdgcn_rsqf(fmaf(sum, a.inv_d, a.eps));
-    if (BF16 && !(sum < __builtin_inff())) {  // squares of bf16 pass fp32: with a factor of 2^-70
+    const float mean = fmaf(sum, a.inv_d, a.eps);
+    float by = __builtin_amdgcn_rsqf(mean);
+    if (BF16 && !(mean < __builtin_inff())) {  // squares of bf16 pass fp32: with a factor of 2^-70
       constexpr float kDown = 0x1p-70f;
       sum = 0.f;
 #pragma unroll
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a) {
         g[i] *= kDown;
         sum = fmaf(f[i], f[i], fmaf(g[i], g[i], sum));
       }
-      by = __builtin_amdgcn_rsqf(group_sum<G>(sum) * a.inv_d);
+      by = __builtin_amdgcn_rsqf(fmaf(group_sum<G>(sum), a.inv_d, a.eps * kDown * kDown));
     }
     if (one)
 #pragma unroll
