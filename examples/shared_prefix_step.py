@@ -5,7 +5,7 @@ Each request has the shared prompt's keys before its own, and brings its last de
     tables = starts, positions, cache rows, tree mask and new pages from the requests' lengths      (step_layout)
     qkv    = x @ dequant(Wqkv)                                                                       (antiquant_matmul)
     q, k normed by head and turned by position; k and v appended to the requests' pages             (norm_rope)
-    attention over the prompt, read once for all requests, and over each one's own pages             (prefix_attention)
+    attention over the prompt, by rows of all requests together, and over each one's own pages       (prefix_attention)
     p      = softmax(attention @ dequant(Wout)), the probabilities after each token                  (antiquant_matmul)
     the drafted tokens that p accepts, and the token that follows                                    (verify_drafts)
 

@@ -201,8 +201,9 @@ int wq_step_layout(const wq_tensor* context_lens, const wq_tensor* new_lens, con
                    const wq_tensor* free_left, void* stream);
 
 /*
- * Attention of a batch whose sequences share long prefixes, each prefix read once for all of
- * its sequences: as wq_tree_attention, but a token of sequence b, prefix_starts[g] <= b <
+ * Attention of a batch whose sequences share long prefixes, each prefix read by rows of all its
+ * sequences together (once for a tile of up to 256 rows, a token's hq / hkv query heads being rows; the tile
+ * follows from N, G and hq / hkv, the rows of the mean prefix; 16 with d = 256): as wq_tree_attention, but a token of sequence b, prefix_starts[g] <= b <
  * prefix_starts[g + 1], sees the prefix_lens[g] keys of prefix g besides, in one softmax with its
  * own.  Key j of prefix g is row prefix_table[g, j / page_size] * page_size + j % page_size of the caches.
  *

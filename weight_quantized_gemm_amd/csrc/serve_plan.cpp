@@ -72,8 +72,8 @@ TreePlan plan_tree(const TreeProblem& p) {
   //   64 rows, 16 sequences: 2 waves 128 us, 4 141 us;  48 rows of 4 cached heads: 74 us, 79 us
   //   112 rows, 16 sequences: 2 waves 155 us, 4 143 us, 8 221 us
   //   256 rows, 16 sequences: 4 waves 240 us, 8 228 us;  512 rows, 8 sequences: 229 us, 218 us
-  // At d = 256 the outputs of a wave of more than 16 rows, or any of the other kernel, would not
-  // fit its registers.
+  // At d = 256 the outputs of a wave of more than 16 rows, or of the other kernel as it stands, whose waves have
+  // 32, would not fit its registers; that kernel with 16 rows a wave was not built.
   const int64_t rows = ceil_div(p.N, std::min(p.N, p.B)) * p.group;
   int per_cu = 1;  // workgroups that a compute unit holds: by LDS, and 8 waves of 256 registers
   if (rows <= 32 || p.d == 256) {

@@ -3,7 +3,10 @@
 //
 // Both parts are the work of serve_tree.hip's kernels.  A prefix is a tile row of its own: all tokens of the
 // group's sequences, times the query heads of a cached head, are the rows that share its keys, so that a prefix is read
-// once for up to 256 rows instead of once for each sequence.  Neither part knows the other: each leaves
+// once for a tile of them instead of once for each sequence.  A tile has up to 256 rows, by those of the mean group
+// (plan_tree), so that one large group beside many small ones reads its prefix more often (48 sequences behind 8000 keys,
+// 4 query heads for a cached one of 128: 56 us; with 16 prefixes of one sequence beside them 90); with heads of
+// 256 it has 16 (32 sequences of 16 tokens behind prefixes of 12001 and 16001, 32 heads for 4: 1870 us, 113 TFLOP/s).  Neither part knows the other: each leaves
 // (output, base, sum) of its rows, and the join adds up a row's parts of both,
 //
 //   out = sum_i 2^(base_i - base) output_i / sum_i 2^(base_i - base) sum_i.

@@ -159,8 +159,9 @@ class PrefixAttention(_Prepared):
 
 def prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, prefix_starts, block_table, context_lens, q_starts,
                      tree_mask=None, *, page_size, scale=None, out=None, workspace=None, stream=None):
-    """:func:`tree_attention` of a batch whose sequences share long prefixes, each of which is read once for all
-    of its sequences.
+    """:func:`tree_attention` of a batch whose sequences share long prefixes, each of which is read by rows of all
+    its sequences together: once for 16, 32, 64, 128 or 256 rows (tokens times the query heads of a cached head) by the mean
+    over the prefixes, with heads of 256 once for 16.
 
     The sequences prefix_starts[g] .. prefix_starts[g+1] (int32 (G + 1)) see, before their own keys, the
     prefix_lens[g] keys (int32 (G)) of prefix g, key j in row prefix_table[g, j // page_size] * page_size + j % page_size
