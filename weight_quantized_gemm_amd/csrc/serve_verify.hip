@@ -23,8 +23,13 @@
 // (1023 refusals over 65536 tokens: 6.6 ms, 6.5 us each; a request's row is not shared among workgroups.)
 //
 // Everything that is compared or summed is fp64, in an order that depends on sizes alone: equal calls give
-// equal tokens, and a token differs from the exact one where the random number is within 2^-50 of a
-// border of its running sums (of V borders, in fp32 one in a hundred calls would be so near).
+// equal tokens.  With e = 2^-53 a running sum goes through at most unit / 64 + unit / 512 + 46 additions (in a lane, across
+// lanes, units and waves, and again inside the unit that is found), its share of the whole through unit / 64 + 21, and the numbers that are
+// summed are off by e each: a token differs from the exact one where the random number is within 2^-46 of a border of the
+// running sums, as a share of the whole (V up to 2^19, unit = 512; 2^-43 at V = 2^24).  In fp32 one call in a hundred
+// would be so near one of V borders.  After two or more refusals C is a sum too: T_i goes through V / 1024 + 23
+// additions, an error of C moves the later T the other way by no more than itself, and so what c refusals leave is off by
+// (V / 1024 + 24 + c) e C / T of itself, which is more where the refusals left little.
 //
 // Bound by two launches and the chain request -> tests -> row -> sums -> unit -> token.  Measured (kernel trace): a chain of
 // 5 over 32000 tokens 3.7 + 3.9 us; 16 trees of 24 4.9 + 5.3; 64 chains of 9 with draft's probabilities, 67 MB read, 12.8
