@@ -152,7 +152,7 @@ int wq_tree_attention(const wq_tensor* q, const wq_tensor* k_cache, const wq_ten
  *   positions  required; WQ_I32; (T), or (A, T) with axes; A in [1, 16].
  *   axes       optional; WQ_I32; (rot/2): the axis of each pair.  A pair whose axis is outside [0, A) does
  *              not turn (its position is 0).  Required with positions of two dimensions.
- *   q_weight   optional; q's dtype or WQ_F32; (d).  Absent: q is not normed.
+ *   q_weight   optional; q's dtype or WQ_F32; (d), its first element 16-byte aligned.  Absent: q is not normed.
  *   k_weight   optional (only with k); the same for k.
  *   eps        finite and at least 2^-126.
  * Sums are fp32 and do not overflow: a head whose squares pass fp32 is taken with a factor.
@@ -180,7 +180,8 @@ int wq_norm_rope(const wq_tensor* q, const wq_tensor* k, const wq_tensor* v, con
  *                others stay.  They come from the top of a stack, free_pages[0 .. free_count), in the
  *                order of the requests and their pages; when it is empty, -1.
  *   free_left    (1): free_count less the pages that were needed; negative: so many were missing.
- * Tokens past the last request's: request -1, slot -1, position 0, mask 0.
+ * Tokens past the last request's: request -1, slot -1, position 0, mask 0.  With parents a token takes a step for each
+ * of its ancestors, one after the other.
  *
  *   context_lens, new_lens  required; (B); B at most 65535.
  *   block_table             required; (B, W), contiguous; W * page_size at most 2^31-2^16; written in place.

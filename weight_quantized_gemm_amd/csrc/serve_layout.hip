@@ -11,7 +11,7 @@
 // their page from the stack themselves and never read what another token writes.
 //
 // Measured (kernel trace): one token of each of 48 requests 4.9 us; 64 trees of up to 48 tokens, with the walks up the
-// parents in LDS, 8.9; 4096 requests of 86237 tokens 7.8, 1.1 MB moved in twice the time of a
+// parents in LDS, 9.2; 4096 requests of 86237 tokens 7.6, 1.1 MB moved in twice the time of a
 // bare launch.
 #include <algorithm>
 

@@ -13,8 +13,11 @@
 // The workgroup computes the cosines and sines of its tokens once, in LDS, for all heads; angles are products in fp64,
 // taken in turns and reduced to half a turn before they become fp32.
 //
-// Measured (kernel trace): 16384 tokens of 32 + 8 + 8 heads of 128 in bf16 80.5 us, 5.0 TB/s of reads and writes, where a
-// copy has 5.2 (87.9 with one piece a lane); 6001 tokens of three axes, interleaved, 26.0 us (4.3 TB/s); 8 tokens 4.2 us.
+// Measured (kernel trace): 16384 tokens of 32 + 8 + 8 heads of 128 in bf16 78.9 us, 5.1 TB/s of reads and writes, where a
+// copy has 5.2 (87.9 with one piece a lane), and 89.0 with 20 elements that turn (kOdd); 6001 tokens of three axes,
+// interleaved, heads of 96, 26.0 us (113 MB at 4.3 TB/s, within the 256 MB cache); 8 tokens 4.2 us.  Without weights this is
+// rope's formula; calls of 16384 tokens as above, in us, rope's kernel first: 128 elements that turn 76.4 and 76.6,
+// interleaved 74.8 and 76.4, 64 elements 81.6 and 75.2, 20 elements 377 and 79.8.
 #include <algorithm>
 
 #include "serve_device.h"

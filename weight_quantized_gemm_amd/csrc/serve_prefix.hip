@@ -15,10 +15,11 @@
 // where the group's tiles begin, which the kernel of the prefix notes for each group.
 //
 // Long prefixes of many rows are bound by the matrix cores and the vector units (serve_tree.hip says how), the own keys
-// by memory, few rows by the launches and the workgroups' starts.  Measured (kernel trace, heads of 128): 32 trees of 16
-// tokens behind two shared prompts of up to 16001, prefix 371 us, own keys 42, join 19 (212 GFLOP: 540 TFLOP/s over the
-// call, 810 with the weights' second terms); 64 single tokens behind 32768, prefix 79, own keys 46, join 11.5; 8 behind
-// 2000, both parts by one launch 16.4, join 6.1.
+// by memory, few rows by the launches and the workgroups' starts.  Measured (kernel trace, after 200 calls, heads of 128): 32
+// trees of 16 tokens behind two shared prompts of up to 16001, prefix 316 us, own keys 40, join 19 (212 GFLOP in 375 us:
+// 565 TFLOP/s, 850 with the weights' second terms); 64 single tokens behind 32768, prefix 66 (520 TFLOP/s), own keys 43 (164 MB
+// at 3.8 TB/s), join 11; 8 behind 2000, both parts by one launch 16.6, join 5.9.  A card that comes from idle takes some 50
+// calls to its full clock: the first 30 of the trees' prefix take 376.
 #include "serve_tree.h"
 #include "serve_step_kernels.h"
 

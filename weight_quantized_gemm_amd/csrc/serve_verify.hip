@@ -32,9 +32,10 @@
 // (V / 1024 + 24 + c) e C / T of itself, which is more where the refusals left little.
 //
 // Bound by two launches and the chain request -> tests -> row -> sums -> unit -> token.  Measured (kernel trace): a chain of
-// 5 over 32000 tokens 3.7 + 3.9 us; 16 trees of 24 4.9 + 5.3; 64 chains of 9 with draft's probabilities, 67 MB read, 12.8
-// (5.2 TB/s) + 7.4.  With running sums of single tokens by the whole workgroup in place of units of 512 the
-// pick took 13 to 15 us.
+// 5 over 32000 tokens 3.7 + 4.0 us; 16 trees of 24 4.9 + 5.4; 64 chains of 9 with draft's probabilities, 67 MB read, 12.9
+// (5.2 TB/s, within the 256 MB cache) + 7.2.  With running sums of single tokens by the whole workgroup in place of units of
+// 512 the pick took 13 to 15 us.  Trees of 24 with draft's probabilities, by three launches: one request over 32000
+// 5.5 + 3.1 + 3.7, 16 over 131072 28.5 (the walk, a workgroup each) + 4.8 + 6.8.
 #include <algorithm>
 
 #include "serve_device.h"

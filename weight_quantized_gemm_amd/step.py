@@ -99,7 +99,7 @@ def norm_rope(q, k, v, positions, inv_freq, *, q_weight=None, k_weight=None, eps
               interleaved=False, attention_factor=1.0, q_out=None, k_out=None, v_out=None, stream=None):
     """:func:`rope` with norms of the heads and positions of several axes, in the same pass and with one rounding.
 
-    q_weight, k_weight: (d), of q's type or fp32: each head x of q (of k) is first x / sqrt(mean(x^2) + eps) *
+    q_weight, k_weight: (d), of q's type or fp32, 16-byte aligned: each head x of q (of k) is first x / sqrt(mean(x^2) + eps) *
     weight; None: q (k) is not normed.  positions: int32 (T), or (A, T) with axes, int32 (rot/2), the axis of each pair
     of elements (:func:`rope_axes`); a pair whose axis is none of the A does not turn.  The other arguments and
     the result are those of :func:`rope`."""
